@@ -16,7 +16,9 @@ import torch
 
 __all__ = ["lib", "fwd", "bwd", "Saved", "SsdError", "make_dims", "num_configs", "config_name",
            "bwd_workspace_size", "fwd_workspace_size", "bwd_num_launches", "bwd_launch_names", "LIB_PATH",
-           "dt_fwd", "dt_bwd", "gate_fwd", "gate_bwd", "conv1d_fwd", "conv1d_bwd", "SSDFunction", "ssd"]
+           "dt_fwd", "dt_bwd", "gate_fwd", "gate_bwd", "conv1d_fwd", "conv1d_bwd", "SSDFunction", "ssd",
+           "qk_fwd", "qk_bwd", "QkFunction", "qk_norm", "delta_fwd", "delta_bwd", "delta_prefill", "delta_step",
+           "DeltaSaved", "DeltaFunction", "delta", "make_delta_dims", "make_qk_dims", "delta_path_name"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmamba2_ssd.so")
 
@@ -122,6 +124,7 @@ def lib():
         L.mamba2_ssd_conv1d_bwd_workspace_size.restype = sz
         L.mamba2_ssd_conv1d_bwd.argtypes = [i64, i64, i64, i32, i32, i32] + [vp] * 9 + [sz, ci, ci, vp]
         L.mamba2_ssd_conv1d_bwd.restype = ci
+        _delta.declare(L)
         _lib = L
     return _lib
 
@@ -434,3 +437,11 @@ class SSDFunction(torch.autograd.Function):
 def ssd(x, dt, A, B, C, D, chunk_size, seq_idx=None, init_states=None, any_start=False):
     """Differentiable Mamba2 SSD chunked scan (see SSDFunction)."""
     return SSDFunction.apply(x, dt, A, B, C, D, chunk_size, seq_idx, init_states, any_start)
+
+
+# ---- gated delta rule, and the norm and rotation of its queries and keys ----
+# (at the end: the module uses the helpers above)
+
+from . import _delta  # noqa: E402
+from ._delta import (DeltaFunction, DeltaSaved, QkFunction, delta, delta_bwd, delta_fwd, delta_path_name,  # noqa: E402
+                     delta_prefill, delta_step, make_delta_dims, make_qk_dims, qk_bwd, qk_fwd, qk_norm)

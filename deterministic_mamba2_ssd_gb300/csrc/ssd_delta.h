@@ -1,0 +1,112 @@
+// ssd_delta.h -- shapes, arguments and kernel families of the gated delta
+// rule, shared by its C entry points and its kernels.
+//
+// Per head, with a (P x N) state S, and per token a log decay g, a step size
+// beta, key k, query q and value v (bars mark the state after the decay):
+//
+//     Sd = exp(g) S;   e = v - Sd k;   S = Sd + beta e k^T;   o = scale S q
+//
+// The backward of L = sum(o * dout), token by token from the last to the
+// first, with dS the gradient of the state after the token:
+//
+//     dS += scale dout q^T;  F = dS k;  dbeta = F . e;  dv = beta F
+//     dk = beta dS^T e - Sd^T dv;  dS -= dv k^T;  dg = <dS, Sd>;  dS *= exp(g)
+//
+// Over a chunk of tokens, with G the running sum of g inside the chunk, S0
+// the state entering it and D_ts = exp(G_t - G_s):
+//
+//     (I + A) E = V - exp(G) K S0^T,  A_ts = D_ts (k_t . k_s) beta_s, s < t
+//     O = scale (exp(G) Q S0^T + (Q K^T o D, s <= t) (beta E))
+//     S1 = exp(G_C) S0 + (exp(G_C - G) beta E)^T K
+//
+// so inside a chunk everything is a product of matrices, and only S is
+// carried from chunk to chunk.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "ssd_common.cuh"
+
+namespace ssd {
+namespace delta {
+
+constexpr int kChunk = 64;      // tokens of a chunk, and the spacing of saved states
+constexpr int kMaxState = 256;  // largest dstate
+
+struct Shape {
+  int64_t T, total;             // tokens of a row (without cu_seqlens), tokens in all
+  int64_t nseq, slots;          // sequences, chunk slots (see chunk_slot)
+  int64_t qs, ks, vs;           // elements between consecutive tokens of q, k, v
+  int H, P, G, N, hpg;
+};
+
+struct Args {
+  const void *q, *k, *v, *dout;
+  const float *g, *beta, *init, *dfinal;
+  const int32_t *cu;            // (nseq + 1) first token of each sequence, or null
+  void *o, *dq, *dk, *dv, *dg, *dbeta;
+  float *fin, *dinit;
+  float scale;
+};
+
+// Where one sequence's tokens are.  A table that is not non-decreasing from 0
+// to total is the caller's mistake; the clamps keep its reads and writes
+// inside the arrays.
+__device__ __forceinline__ void seq_range(const Shape &s, const int32_t *cu, int64_t i, int64_t &b, int64_t &e) {
+  if (cu == nullptr) {
+    b = i * s.T;
+    e = b + s.T;
+  } else {
+    b = min(max(int64_t(cu[i]), int64_t(0)), s.total);
+    e = min(max(int64_t(cu[i + 1]), b), s.total);
+  }
+}
+
+// Chunks are counted from each sequence's own first token.  Chunk j of
+// sequence i has slot floor(start_i / 64) + i + j: ceil(len / 64) slots fit
+// between one sequence's first slot and the next one's, so no table is needed.
+__host__ __device__ __forceinline__ int64_t chunk_slots(const int64_t total, const int64_t T, const int64_t nseq,
+                                                        bool packed) {
+  return packed ? total / kChunk + nseq : nseq * ((T + kChunk - 1) / kChunk);
+}
+__device__ __forceinline__ int64_t first_slot(const Shape &s, const int32_t *cu, int64_t i, int64_t b) {
+  return cu == nullptr ? i * ((s.T + kChunk - 1) / kChunk) : b / kChunk + i;
+}
+
+// Sequence and tokens [b, e) of a slot; false for a slot that holds no chunk.
+__device__ __forceinline__ bool chunk_of_slot(const Shape &s, const int32_t *cu, int64_t slot, int64_t &seq, int64_t &b,
+                                              int64_t &e) {
+  int64_t sb, se;
+  if (cu == nullptr) {
+    seq = slot / ((s.T + kChunk - 1) / kChunk);
+    seq_range(s, cu, seq, sb, se);
+  } else {
+    int64_t lo = 0, hi = s.nseq - 1;   // last sequence whose first slot is <= slot
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) >> 1;
+      seq_range(s, cu, mid, sb, se);
+      if (sb / kChunk + mid <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    seq = lo;
+    seq_range(s, cu, seq, sb, se);
+  }
+  b = sb + (slot - first_slot(s, cu, seq, sb)) * kChunk;
+  e = min(b + kChunk, se);
+  return b >= sb && b < e;
+}
+
+// General path (fp32 or bf16, any headdim, dstate <= kMaxState): CUDA cores, token by token, fp32 throughout.
+// saved: states entering each chunk (slots, H, P, N) and e (total, H, P), fp32.
+size_t general_saved(const Shape &s);
+size_t general_bwd_workspace(const Shape &s);
+cudaError_t general_fwd(const Shape &s, bool bf16, const Args &a, void *saved, cudaStream_t st);
+cudaError_t general_bwd(const Shape &s, bool bf16, const Args &a, const void *saved, void *ws, cudaStream_t st);
+// Recurrent form on a pool of states (nslots, H, P, N), updated in place; s.nseq rows of s.T tokens.
+cudaError_t general_step(const Shape &s, bool bf16, const Args &a, float *pool, const int32_t *slots, int64_t nslots,
+                         cudaStream_t st);
+
+}  // namespace delta
+}  // namespace ssd

@@ -1,0 +1,148 @@
+// ssd_delta_api.cu -- C entry points of the gated delta rule: argument
+// checks, sizes and the choice of the kernels.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "mamba2_ssd.h"
+#include "ssd_delta.h"
+
+namespace {
+
+using ssd::delta::Args;
+using ssd::delta::Shape;
+
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool dims_ok(const ssd_delta_dims *d) {
+  if (d == nullptr) return false;
+  if (d->batch < 1 || d->seqlen < 0 || d->nheads < 1 || d->headdim < 1 || d->ngroups < 1 || d->dstate < 1 ||
+      d->nseq < 1)
+    return false;
+  if (d->nheads % d->ngroups != 0 || d->nheads > 65535 || d->headdim > 65535 || d->dstate > ssd::delta::kMaxState)
+    return false;
+  if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return false;
+  if ((d->flags & ~SSD_DELTA_CU_SEQLENS) != 0) return false;
+  if (d->flags & SSD_DELTA_CU_SEQLENS) {
+    if (d->batch != 1) return false;   // packed: one row
+  } else if (d->nseq != d->batch) {
+    return false;
+  }
+  const int64_t top = int64_t(1) << 31;
+  if (d->batch >= top || d->seqlen >= top || d->nseq >= top || d->batch * (d->seqlen + 1) >= top) return false;
+  const int64_t qk = d->ngroups * d->dstate, v = d->nheads * d->headdim, far = int64_t(1) << 31;
+  if (d->q_stride < 0 || d->k_stride < 0 || d->v_stride < 0 || d->q_stride > far || d->k_stride > far ||
+      d->v_stride > far)
+    return false;
+  if ((d->q_stride != 0 && d->q_stride < qk) || (d->k_stride != 0 && d->k_stride < qk) ||
+      (d->v_stride != 0 && d->v_stride < v))
+    return false;
+  return true;
+}
+
+Shape shape_of(const ssd_delta_dims *d) {
+  Shape s;
+  s.T = d->seqlen;
+  s.total = d->batch * d->seqlen;
+  s.nseq = d->nseq;
+  s.slots = ssd::delta::chunk_slots(s.total, s.T, s.nseq, (d->flags & SSD_DELTA_CU_SEQLENS) != 0);
+  s.H = int(d->nheads);
+  s.P = int(d->headdim);
+  s.G = int(d->ngroups);
+  s.N = int(d->dstate);
+  s.hpg = s.H / s.G;
+  s.qs = d->q_stride ? d->q_stride : int64_t(s.G) * s.N;
+  s.ks = d->k_stride ? d->k_stride : int64_t(s.G) * s.N;
+  s.vs = d->v_stride ? d->v_stride : int64_t(s.H) * s.P;
+  return s;
+}
+
+bool bf16_of(const ssd_delta_dims *d) { return d->dtype == SSD_BF16; }
+
+// Activations need their own element's alignment only: heads and rows may lie anywhere in a projection's output.
+bool acts_ok(const ssd_delta_dims *d, std::initializer_list<const void *> ps) {
+  for (const void *p : ps)
+    if (p == nullptr || !aligned(p, bf16_of(d) ? 2 : 4)) return false;
+  return true;
+}
+bool floats_ok(std::initializer_list<const void *> ps) {
+  for (const void *p : ps)
+    if (p == nullptr || !aligned(p, 4)) return false;
+  return true;
+}
+
+ssd_status status_of(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+size_t mamba2_ssd_delta_saved_size(const ssd_delta_dims *dims) {
+  return dims_ok(dims) ? ssd::delta::general_saved(shape_of(dims)) + 256 : 0;
+}
+
+size_t mamba2_ssd_delta_fwd_workspace_size(const ssd_delta_dims *dims) { return dims_ok(dims) ? 256 : 0; }
+
+size_t mamba2_ssd_delta_bwd_workspace_size(const ssd_delta_dims *dims) {
+  return dims_ok(dims) ? ssd::delta::general_bwd_workspace(shape_of(dims)) + 256 : 0;
+}
+
+const char *mamba2_ssd_delta_path_name(const ssd_delta_dims *dims) { return dims_ok(dims) ? "general" : "invalid"; }
+
+ssd_status mamba2_ssd_delta_fwd(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                                const float *beta, const int32_t *cu_seqlens, const float *init_states, float scale,
+                                void *o, float *final_states, void *saved, size_t saved_bytes, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+  if (!dims_ok(dims) || !isfinite(scale)) return SSD_ERR_INVALID_ARG;
+  const Shape s = shape_of(dims);
+  if (((dims->flags & SSD_DELTA_CU_SEQLENS) != 0) != (cu_seqlens != nullptr) || !aligned(cu_seqlens, 4))
+    return SSD_ERR_INVALID_ARG;
+  if (!aligned(init_states, 16) || !aligned(final_states, 16) || !aligned(saved, 16) || !aligned(workspace, 16))
+    return SSD_ERR_INVALID_ARG;
+  if (s.total > 0 && (!acts_ok(dims, {q, k, v, o}) || !floats_ok({g, beta}))) return SSD_ERR_INVALID_ARG;
+  if (saved != nullptr && saved_bytes < mamba2_ssd_delta_saved_size(dims)) return SSD_ERR_WORKSPACE;
+  if (workspace_bytes < mamba2_ssd_delta_fwd_workspace_size(dims)) return SSD_ERR_WORKSPACE;
+  if (workspace == nullptr) return SSD_ERR_INVALID_ARG;
+  Args a{};
+  a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.cu = cu_seqlens, a.init = init_states, a.o = o;
+  a.fin = final_states, a.scale = scale;
+  return status_of(ssd::delta::general_fwd(s, bf16_of(dims), a, saved, static_cast<cudaStream_t>(stream)));
+}
+
+ssd_status mamba2_ssd_delta_bwd(const ssd_delta_dims *dims, const void *q, const void *k, const float *g,
+                                const float *beta, const int32_t *cu_seqlens, float scale, const void *saved,
+                                size_t saved_bytes, const void *dout, const float *dfinal, void *dq, void *dk, void *dv,
+                                void *dg, void *dbeta, float *dinit, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+  if (!dims_ok(dims) || !isfinite(scale)) return SSD_ERR_INVALID_ARG;
+  const Shape s = shape_of(dims);
+  if (((dims->flags & SSD_DELTA_CU_SEQLENS) != 0) != (cu_seqlens != nullptr) || !aligned(cu_seqlens, 4))
+    return SSD_ERR_INVALID_ARG;
+  if (saved == nullptr || !aligned(saved, 16) || !aligned(dfinal, 16) || !aligned(dinit, 16) || workspace == nullptr ||
+      !aligned(workspace, 16))
+    return SSD_ERR_INVALID_ARG;
+  if (s.total > 0 && (!acts_ok(dims, {q, k, dout, dq, dk, dv, dg, dbeta}) || !floats_ok({g, beta})))
+    return SSD_ERR_INVALID_ARG;
+  if (saved_bytes < mamba2_ssd_delta_saved_size(dims)) return SSD_ERR_WORKSPACE;
+  if (workspace_bytes < mamba2_ssd_delta_bwd_workspace_size(dims)) return SSD_ERR_WORKSPACE;
+  Args a{};
+  a.q = q, a.k = k, a.g = g, a.beta = beta, a.cu = cu_seqlens, a.scale = scale, a.dout = dout, a.dfinal = dfinal;
+  a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dinit = dinit;
+  return status_of(ssd::delta::general_bwd(s, bf16_of(dims), a, saved, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+ssd_status mamba2_ssd_delta_step(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                                 const float *beta, float scale, float *states, int64_t num_slots, const int32_t *slots,
+                                 void *o, void *stream) {
+  if (!dims_ok(dims) || !isfinite(scale) || (dims->flags & SSD_DELTA_CU_SEQLENS)) return SSD_ERR_INVALID_ARG;
+  const Shape s = shape_of(dims);
+  if (num_slots < 1 || (slots == nullptr && num_slots < s.nseq) || !aligned(slots, 4)) return SSD_ERR_INVALID_ARG;
+  if (s.total == 0) return SSD_OK;
+  if (states == nullptr || !aligned(states, 16) || !acts_ok(dims, {q, k, v, o}) || !floats_ok({g, beta}))
+    return SSD_ERR_INVALID_ARG;
+  Args a{};
+  a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.o = o, a.scale = scale;
+  return status_of(
+      ssd::delta::general_step(s, bf16_of(dims), a, states, slots, num_slots, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

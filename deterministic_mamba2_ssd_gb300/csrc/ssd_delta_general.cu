@@ -1,0 +1,589 @@
+// ssd_delta_general.cu -- gated delta rule on CUDA cores: the recurrent
+// forward (whole sequences, and the in-place update of a pool of states that
+// serves single tokens), the recurrent backward of the state, and the chunk
+// kernel that turns both into the gradients.  fp32 arithmetic throughout, any
+// headdim, dstate up to 256.
+//
+// Rows of the state never mix: row p of S sees only v[p].  So a row is the
+// unit of work: 8 lanes share one, four rows a warp, sixteen a CTA, and the
+// state stays in registers over the whole sequence.  Per token and row two
+// products over dstate (S k, S q), each summed inside the 8 lanes by three
+// shuffles in one fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ssd_delta.h"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+constexpr int kRows = 16;      // state rows of a CTA
+constexpr int kBlock = 8;      // tokens staged in shared memory at a time
+constexpr int kThreads = 128;
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Sum over the 8 lanes that share a row; every lane gets it.
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) v += __shfl_xor_sync(~0u, v, d);
+  return v;
+}
+
+// The state row of this lane: columns (8 j + lane8) * 4 + i, zero past N.
+template <int NJ>
+__device__ __forceinline__ void load_row(float (&s)[4 * NJ], const float *row, int N, int lane8) {
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int c = (8 * j + lane8) * 4;
+    if ((N & 3) == 0) {
+      const float4 v = row != nullptr && c < N ? *reinterpret_cast<const float4 *>(row + c) : make_float4(0, 0, 0, 0);
+      s[4 * j] = v.x;
+      s[4 * j + 1] = v.y;
+      s[4 * j + 2] = v.z;
+      s[4 * j + 3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[4 * j + i] = row != nullptr && c + i < N ? row[c + i] : 0.f;
+    }
+  }
+}
+template <int NJ>
+__device__ __forceinline__ void store_row(const float (&s)[4 * NJ], float *row, int N, int lane8) {
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int c = (8 * j + lane8) * 4;
+    if ((N & 3) == 0) {
+      if (c < N) *reinterpret_cast<float4 *>(row + c) = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < N) row[c + i] = s[4 * j + i];
+    }
+  }
+}
+
+// One block of tokens on its way to shared memory: first every load into
+// registers (while the block before is being worked on), then the stores.
+template <class T, int NJ, bool kBwd>
+struct Stage {
+  static constexpr int kWide = 32 * NJ;                       // padded dstate
+  static constexpr int kVec = kBlock * kWide / kThreads;      // q (and k) elements of a thread
+  float q[kVec], k[kVec], v, d, g, b;
+
+  __device__ __forceinline__ void load(const Shape &s, const Args &a, int64_t t0, int64_t e, int h, int p0) {
+    const int grp = h / s.hpg;
+    const T *qp = static_cast<const T *>(a.q) + int64_t(grp) * s.N, *kp = static_cast<const T *>(a.k) + int64_t(grp) * s.N;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int x = threadIdx.x + i * kThreads, c = x % kWide;
+      const int64_t t = t0 + x / kWide;
+      const bool in = t < e && c < s.N;
+      q[i] = in ? ld(qp + t * s.qs + c) : 0.f;
+      k[i] = in ? ld(kp + t * s.ks + c) : 0.f;
+    }
+    const int64_t t = t0 + threadIdx.x / kRows;
+    const int p = p0 + threadIdx.x % kRows;
+    const bool in = t < e && p < s.P;
+    if (!kBwd) v = in ? ld(static_cast<const T *>(a.v) + t * s.vs + int64_t(h) * s.P + p) : 0.f;
+    if (kBwd) d = in ? ld(static_cast<const T *>(a.dout) + (t * s.H + h) * s.P + p) : 0.f;
+    const int64_t tg = t0 + threadIdx.x;
+    const bool ing = threadIdx.x < kBlock && tg < e;
+    g = ing ? expf(a.g[tg * s.H + h]) : 1.f;    // a token past the end leaves the state as it is
+    b = ing ? a.beta[tg * s.H + h] : 0.f;
+  }
+};
+
+template <int NJ>
+struct Tile {
+  float q[kBlock][32 * NJ], k[kBlock][32 * NJ];
+  float x[kBlock][kRows];      // v (forward) or dout (backward)
+  float y[kBlock][kRows];      // o (forward) or F (backward)
+  float z[kBlock][kRows];      // e (forward)
+  float g[kBlock], b[kBlock];
+
+  template <class T, bool kBwd>
+  __device__ __forceinline__ void put(const Stage<T, NJ, kBwd> &st) {
+#pragma unroll
+    for (int i = 0; i < Stage<T, NJ, kBwd>::kVec; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      (&q[0][0])[e] = st.q[i];
+      (&k[0][0])[e] = st.k[i];
+    }
+    (&x[0][0])[threadIdx.x] = kBwd ? st.d : st.v;
+    if (threadIdx.x < kBlock) {
+      g[threadIdx.x] = st.g;
+      b[threadIdx.x] = st.b;
+    }
+  }
+};
+
+// CTA (16 rows of the state, head, sequence), tokens in order.
+template <class T, int NJ, bool kPool>
+__global__ void __launch_bounds__(kThreads) rec_fwd_kernel(Shape s, Args a, float *__restrict__ states,
+                                                           float *__restrict__ es, float *__restrict__ pool,
+                                                           const int32_t *__restrict__ slots, int64_t nslots) {
+  __shared__ Tile<NJ> sm;
+  const int lane8 = threadIdx.x & 7, r = threadIdx.x >> 3;
+  const int p0 = blockIdx.x * kRows, p = p0 + r, h = blockIdx.y;
+  const bool live = p < s.P;
+  T *o = static_cast<T *>(a.o);
+  for (int64_t seq = blockIdx.z; seq < s.nseq; seq += gridDim.z) {
+    int64_t t0, te;
+    seq_range(s, a.cu, seq, t0, te);
+    int64_t at = seq;
+    if (kPool) {
+      if (slots != nullptr) at = slots[seq];
+      if (at < 0 || at >= nslots) {   // an idle row: nothing is read or kept for it
+        for (int64_t x = threadIdx.x; x < s.T * kRows; x += kThreads) {
+          const int pp = p0 + int(x % kRows);
+          if (pp < s.P) o[((t0 + x / kRows) * s.H + h) * s.P + pp] = from_f32<T>(0.f);
+        }
+        continue;
+      }
+    }
+    const float *from = kPool ? pool : a.init;
+    float *to = kPool ? pool : a.fin;
+    const int64_t row = ((at * s.H + h) * s.P + p) * s.N;
+    float S[4 * NJ];
+    load_row<NJ>(S, live && from != nullptr ? from + row : nullptr, s.N, lane8);
+    const int64_t slot0 = kPool ? 0 : first_slot(s, a.cu, seq, t0);
+    Stage<T, NJ, false> st;
+    if (t0 < te) st.load(s, a, t0, te, h, p0);
+    for (int64_t b0 = t0; b0 < te; b0 += kBlock) {
+      if (!kPool && states != nullptr && live && (b0 - t0) % kChunk == 0) {
+        const int64_t slot = slot0 + (b0 - t0) / kChunk;
+        if (slot < s.slots) store_row<NJ>(S, states + ((slot * s.H + h) * s.P + p) * s.N, s.N, lane8);
+      }
+      sm.put(st);
+      __syncthreads();
+      if (b0 + kBlock < te) st.load(s, a, b0 + kBlock, te, h, p0);
+      const int n = int(min(int64_t(kBlock), te - b0));
+      for (int t = 0; t < n; ++t) {
+        float kk[4 * NJ], part = 0.f, out = 0.f;
+        const float dec = sm.g[t];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[t][(8 * j + lane8) * 4]);
+          kk[4 * j] = kv.x;
+          kk[4 * j + 1] = kv.y;
+          kk[4 * j + 2] = kv.z;
+          kk[4 * j + 3] = kv.w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            S[4 * j + i] *= dec;
+            part = fmaf(S[4 * j + i], kk[4 * j + i], part);
+          }
+        }
+        const float e = sm.x[t][r] - row_sum(part);
+        const float u = sm.b[t] * e;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[t][(8 * j + lane8) * 4]);
+          const float qq[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            S[4 * j + i] = fmaf(u, kk[4 * j + i], S[4 * j + i]);
+            out = fmaf(S[4 * j + i], qq[i], out);
+          }
+        }
+        out = row_sum(out);
+        if (lane8 == 0) {
+          sm.y[t][r] = a.scale * out;
+          sm.z[t][r] = e;
+        }
+      }
+      __syncthreads();
+      const int tt = threadIdx.x / kRows, rr = threadIdx.x % kRows;
+      if (tt < n && p0 + rr < s.P) {
+        const int64_t x = ((b0 + tt) * s.H + h) * s.P + p0 + rr;
+        o[x] = from_f32<T>(sm.y[tt][rr]);
+        if (es != nullptr) es[x] = sm.z[tt][rr];
+      }
+    }
+    if (live && to != nullptr) store_row<NJ>(S, to + row, s.N, lane8);
+    __syncthreads();
+  }
+}
+
+// The reverse recurrence of dS, tokens from the last to the first: writes the
+// gradient of the state leaving each chunk, F, dv and the gradient of the
+// initial state.
+template <class T, int NJ>
+__global__ void __launch_bounds__(kThreads) rec_bwd_kernel(Shape s, Args a, float *__restrict__ dstates,
+                                                           float *__restrict__ F) {
+  __shared__ Tile<NJ> sm;
+  const int lane8 = threadIdx.x & 7, r = threadIdx.x >> 3;
+  const int p0 = blockIdx.x * kRows, p = p0 + r, h = blockIdx.y;
+  const bool live = p < s.P;
+  T *dv = static_cast<T *>(a.dv);
+  for (int64_t seq = blockIdx.z; seq < s.nseq; seq += gridDim.z) {
+    int64_t t0, te;
+    seq_range(s, a.cu, seq, t0, te);
+    const int64_t row = ((seq * s.H + h) * s.P + p) * s.N;
+    float S[4 * NJ];
+    load_row<NJ>(S, live && a.dfinal != nullptr ? a.dfinal + row : nullptr, s.N, lane8);
+    const int64_t slot0 = first_slot(s, a.cu, seq, t0);
+    const int64_t nb = (te - t0 + kBlock - 1) / kBlock;
+    Stage<T, NJ, true> st;
+    if (nb > 0) st.load(s, a, t0 + (nb - 1) * kBlock, te, h, p0);
+    for (int64_t blk = nb - 1; blk >= 0; --blk) {
+      const int64_t b0 = t0 + blk * kBlock;
+      if (live && (blk == nb - 1 || (blk + 1) % (kChunk / kBlock) == 0)) {
+        const int64_t slot = slot0 + blk / (kChunk / kBlock);
+        if (slot < s.slots) store_row<NJ>(S, dstates + ((slot * s.H + h) * s.P + p) * s.N, s.N, lane8);
+      }
+      sm.put(st);
+      __syncthreads();
+      if (blk > 0) st.load(s, a, b0 - kBlock, te, h, p0);
+      const int n = int(min(int64_t(kBlock), te - b0));
+      for (int t = n - 1; t >= 0; --t) {
+        float kk[4 * NJ], part = 0.f;
+        const float dec = sm.g[t], d = a.scale * sm.x[t][r];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[t][(8 * j + lane8) * 4]);
+          const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[t][(8 * j + lane8) * 4]);
+          kk[4 * j] = kv.x;
+          kk[4 * j + 1] = kv.y;
+          kk[4 * j + 2] = kv.z;
+          kk[4 * j + 3] = kv.w;
+          const float qq[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            S[4 * j + i] = fmaf(d, qq[i], S[4 * j + i]);
+            part = fmaf(S[4 * j + i], kk[4 * j + i], part);
+          }
+        }
+        const float f = row_sum(part);
+        const float de = sm.b[t] * f;
+#pragma unroll
+        for (int i = 0; i < 4 * NJ; ++i) S[i] = dec * fmaf(-de, kk[i], S[i]);
+        if (lane8 == 0) sm.y[t][r] = f;
+      }
+      __syncthreads();
+      const int tt = threadIdx.x / kRows, rr = threadIdx.x % kRows;
+      if (tt < n && p0 + rr < s.P) {
+        const int64_t x = ((b0 + tt) * s.H + h) * s.P + p0 + rr;
+        const float f = sm.y[tt][rr];
+        F[x] = f;
+        dv[x] = from_f32<T>(sm.b[tt] * f);
+      }
+      __syncthreads();
+    }
+    if (live && a.dinit != nullptr) store_row<NJ>(S, a.dinit + row, s.N, lane8);
+  }
+}
+
+// ---- gradients of a chunk ---------------------------------------------------
+
+constexpr int kGThreads = 256;
+constexpr int kKB = 16;   // contraction elements staged at a time
+
+struct GradTile {
+  float m1[kChunk][kChunk + 1], m2[kChunk][kChunk + 1];   // weights of k_s in up_t and dq_t
+  float a[kKB][kChunk + 4], b[kKB][kChunk + 4];
+  float G[kChunk], Gl[kChunk], beta[kChunk], dG[kChunk], db[kChunk];
+  float red[kGThreads / 32];
+};
+
+// acc[4][4] += sum_k fa(row, k) fb(k, col) for this thread's rows 4 (tid / 16)
+// and columns 4 (tid % 16) of a 64 x 64 tile; kA, kB: the operand is
+// contiguous along the contraction (the loads follow that direction).
+template <bool kA, bool kB, class FA, class FB>
+__device__ __forceinline__ void product(GradTile &sm, float (&acc)[4][4], int K, FA fa, FB fb) {
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  for (int k0 = 0; k0 < K; k0 += kKB) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kChunk * kKB / kGThreads; ++i) {
+      const int x = tid + i * kGThreads;
+      const int ka = kA ? x % kKB : x / kChunk, ra = kA ? x / kKB : x % kChunk;
+      const int kb = kB ? x % kKB : x / kChunk, cb = kB ? x / kKB : x % kChunk;
+      sm.a[ka][ra] = k0 + ka < K ? fa(ra, k0 + ka) : 0.f;
+      sm.b[kb][cb] = k0 + kb < K ? fb(k0 + kb, cb) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kKB; ++k) {
+      const float4 av = *reinterpret_cast<const float4 *>(&sm.a[k][4 * ty]);
+      const float4 bv = *reinterpret_cast<const float4 *>(&sm.b[k][4 * tx]);
+      const float ar[4] = {av.x, av.y, av.z, av.w}, br[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ar[i], br[j], acc[i][j]);
+    }
+  }
+}
+
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v += __shfl_xor_sync(~0u, v, d);
+  return v;
+}
+
+// CTA (chunk slot, head).  With dR = beta F and the chunk's matrices
+//   N1 = dR E^T, N2 = scale dout E^T, M1 = -N1 o D beta (s < t), M2 = N2 o D beta (s <= t):
+//   dq   = scale exp(G) dout S0 + M2 K
+//   up   = M1 K - exp(G) dR S0                       (k_t as the token's own key)
+//   down = M1^T K + M2^T Q + exp(G_C - G) beta E dS  (k_s as written into the state)
+//   dk   = up + down,  dG_t = q_t.dq_t + k_t.up_t - k_t.down_t,
+//   dG_C += exp(G_C) <S0, dS> + sum_s k_s . (last term of down_s),  dg = suffix sums of dG
+// dq and dk of each head go to their own slot; shared_kernel sums the group.
+template <class T>
+__global__ void __launch_bounds__(kGThreads) grads_kernel(Shape s, Args a, const float *__restrict__ states,
+                                                          const float *__restrict__ es,
+                                                          const float *__restrict__ dstates,
+                                                          const float *__restrict__ F, float *__restrict__ dqh,
+                                                          float *__restrict__ dkh) {
+  __shared__ GradTile sm;
+  const int h = blockIdx.y, grp = h / s.hpg, tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  for (int64_t slot = blockIdx.x; slot < s.slots; slot += gridDim.x) {
+    int64_t seq, b, e;
+    if (!chunk_of_slot(s, a.cu, slot, seq, b, e)) continue;
+    const int n = int(e - b);
+    __syncthreads();
+    if (tid < kChunk) {
+      sm.beta[tid] = tid < n ? a.beta[(b + tid) * s.H + h] : 0.f;
+      sm.dG[tid] = sm.db[tid] = 0.f;
+    }
+    if (tid == 0) {   // running sums of g as hi + lo; a decay to nothing stays finite
+      float hi = 0.f, lo = 0.f;
+      for (int t = 0; t < kChunk; ++t) {
+        const float x = t < n ? fmaxf(a.g[(b + t) * s.H + h], -1e4f) : 0.f;
+        const float sum = hi + x, bb = sum - hi;
+        lo += (hi - (sum - bb)) + (x - bb);
+        hi = sum;
+        sm.G[t] = hi;
+        sm.Gl[t] = lo;
+      }
+    }
+    __syncthreads();
+    const T *q = static_cast<const T *>(a.q) + b * s.qs + int64_t(grp) * s.N;
+    const T *k = static_cast<const T *>(a.k) + b * s.ks + int64_t(grp) * s.N;
+    const int64_t tok = b * s.H + h;
+    const T *go = static_cast<const T *>(a.dout) + tok * s.P;
+    const float *E = es + tok * s.P, *Fh = F + tok * s.P;
+    const float *S0 = states + (slot * s.H + h) * s.P * s.N, *dS = dstates + (slot * s.H + h) * s.P * s.N;
+    const int64_t step = int64_t(s.H) * s.P;
+    const float scale = a.scale;
+    auto qv = [&](int t, int c) { return t < n && c < s.N ? ld(q + t * s.qs + c) : 0.f; };
+    auto kv = [&](int t, int c) { return t < n && c < s.N ? ld(k + t * s.ks + c) : 0.f; };
+    auto Ev = [&](int t, int p) { return t < n ? E[t * step + p] : 0.f; };
+    auto dR = [&](int t, int p) { return t < n ? sm.beta[t] * Fh[t * step + p] : 0.f; };
+    auto dO = [&](int t, int p) { return t < n ? scale * ld(go + t * step + p) : 0.f; };
+    {
+      float n1[4][4] = {}, n2[4][4] = {};
+      product<true, true>(sm, n1, s.P, dR, [&](int p, int c) { return Ev(c, p); });
+      product<true, true>(sm, n2, s.P, dO, [&](int p, int c) { return Ev(c, p); });
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = 4 * ty + i, c = 4 * tx + j;
+          const float w = c <= t ? expf(acs_diff(sm.G[t], sm.Gl[t], sm.G[c], sm.Gl[c])) * sm.beta[c] : 0.f;
+          sm.m1[t][c] = c < t ? -n1[i][j] * w : 0.f;
+          sm.m2[t][c] = n2[i][j] * w;
+        }
+    }
+    // dbeta_t = F_t . e_t, one row for each group of four threads
+    {
+      float v = 0.f;
+      const int t = tid / 4;
+      if (t < n)
+        for (int p = tid % 4; p < s.P; p += 4) v = fmaf(Fh[t * step + p], E[t * step + p], v);
+      v += __shfl_xor_sync(~0u, v, 1);
+      v += __shfl_xor_sync(~0u, v, 2);
+      if (tid % 4 == 0) sm.db[t] = v;
+    }
+    __syncthreads();
+    const float GC = sm.G[kChunk - 1], GCl = sm.Gl[kChunk - 1];
+    float tail = 0.f;   // this thread's share of sum_s k_s . state_s
+    float rowsum[4] = {};
+    for (int n0 = 0; n0 < s.N; n0 += kChunk) {
+      auto col = [&](const float *X) {
+        return [&, X](int p, int c) { return n0 + c < s.N ? X[int64_t(p) * s.N + n0 + c] : 0.f; };
+      };
+      auto kcol = [&](int t, int c) { return kv(t, n0 + c); };
+      float dq[4][4] = {}, up[4][4] = {}, down[4][4] = {};
+      product<true, false>(sm, dq, s.P, dO, col(S0));
+      product<true, false>(sm, up, s.P, dR, col(S0));
+      product<true, false>(sm, down, s.P, Ev, col(dS));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * ty + i;
+        const float eg = expf(sm.G[t] + sm.Gl[t]);
+        const float w = expf(acs_diff(GC, GCl, sm.G[t], sm.Gl[t])) * sm.beta[t];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dq[i][j] *= eg;
+          up[i][j] *= -eg;
+          down[i][j] *= w;
+          tail = fmaf(kv(t, n0 + 4 * tx + j), down[i][j], tail);
+        }
+      }
+      product<false, false>(sm, dq, n, [&](int t, int c) { return sm.m2[t][c]; }, kcol);
+      product<false, false>(sm, up, n, [&](int t, int c) { return sm.m1[t][c]; }, kcol);
+      product<false, false>(sm, down, n, [&](int t, int c) { return sm.m1[c][t]; }, kcol);
+      product<false, false>(sm, down, n, [&](int t, int c) { return sm.m2[c][t]; },
+                            [&](int t, int c) { return qv(t, n0 + c); });
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * ty + i;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = n0 + 4 * tx + j;
+          if (t < n && c < s.N) {
+            const float kt = kv(t, c);
+            rowsum[i] = fmaf(qv(t, c), dq[i][j], rowsum[i]);
+            rowsum[i] = fmaf(kt, up[i][j] - down[i][j], rowsum[i]);
+            dqh[((b + t) * s.H + h) * s.N + c] = dq[i][j];
+            dkh[((b + t) * s.H + h) * s.N + c] = up[i][j] + down[i][j];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = half_warp_sum(rowsum[i]);
+      if (tx == 0) sm.dG[4 * ty + i] = v;
+    }
+    // <S0, dS> and the tail terms, both of the chunk's last running sum
+    float inner = 0.f;
+    bool some = false;
+    for (int x = tid; x < s.P * s.N; x += kGThreads) {
+      some |= S0[x] != 0.f;
+      inner = fmaf(S0[x], dS[x], inner);
+    }
+    float tot = fmaf(expf(GC + GCl), inner, tail);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) tot += __shfl_xor_sync(~0u, tot, d);
+    if ((tid & 31) == 0) sm.red[tid >> 5] = tot;
+    some = __syncthreads_or(some);
+    if (tid == 0) {
+      float acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kGThreads / 32; ++w) acc += sm.red[w];
+      for (int t = n - 1; t >= 0; --t) {
+        acc += sm.dG[t];
+        sm.dG[t] = acc;
+      }
+      // the first decay multiplies S0 alone: where that is zero the terms above cancel but for their rounding
+      if (!some) sm.dG[0] = 0.f;
+    }
+    __syncthreads();
+    if (tid < n) {
+      static_cast<T *>(a.dg)[(b + tid) * s.H + h] = from_f32<T>(sm.dG[tid]);
+      static_cast<T *>(a.dbeta)[(b + tid) * s.H + h] = from_f32<T>(sm.db[tid]);
+    }
+  }
+}
+
+// dq, dk of a group: the heads' slots added in ascending order, rounded once.
+template <class T>
+__global__ void shared_kernel(Shape s, const float *__restrict__ dqh, const float *__restrict__ dkh, T *__restrict__ dq,
+                              T *__restrict__ dk) {
+  const int64_t total = s.total * s.G * s.N, stride = int64_t(gridDim.x) * blockDim.x;
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
+    const int64_t c = i % s.N, tg = i / s.N;   // tg = token * G + group, head 0 of it = tg * hpg
+    float x = 0.f, y = 0.f;
+    for (int j = 0; j < s.hpg; ++j) {
+      x += dqh[(tg * s.hpg + j) * s.N + c];
+      y += dkh[(tg * s.hpg + j) * s.N + c];
+    }
+    dq[i] = from_f32<T>(x);
+    dk[i] = from_f32<T>(y);
+  }
+}
+
+struct Saved {
+  float *states, *es;
+  size_t bytes;
+};
+Saved carve_saved(const Shape &s, void *p) {
+  Carver c(p);
+  Saved o;
+  o.states = c.take<float>(s.slots * s.H * s.P * s.N);
+  o.es = c.take<float>(s.total * s.H * s.P);
+  o.bytes = c.bytes();
+  return o;
+}
+struct Work {
+  float *dstates, *F, *dqh, *dkh;
+  size_t bytes;
+};
+Work carve_work(const Shape &s, void *p) {
+  Carver c(p);
+  Work o;
+  o.dstates = c.take<float>(s.slots * s.H * s.P * s.N);
+  o.F = c.take<float>(s.total * s.H * s.P);
+  o.dqh = c.take<float>(s.total * s.H * s.N);
+  o.dkh = c.take<float>(s.total * s.H * s.N);
+  o.bytes = c.bytes();
+  return o;
+}
+
+dim3 rec_grid(const Shape &s) {
+  return dim3(unsigned((s.P + kRows - 1) / kRows), unsigned(s.H), unsigned(s.nseq < 65535 ? s.nseq : 65535));
+}
+
+template <class T, bool kPool>
+cudaError_t launch_fwd(const Shape &s, const Args &a, float *states, float *es, float *pool, const int32_t *slots,
+                       int64_t nslots, cudaStream_t st) {
+  const dim3 grid = rec_grid(s);
+  if (s.N <= 32) rec_fwd_kernel<T, 1, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  else if (s.N <= 64) rec_fwd_kernel<T, 2, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  else if (s.N <= 128) rec_fwd_kernel<T, 4, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  else rec_fwd_kernel<T, 8, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_bwd(const Shape &s, const Args &a, const Saved &sv, const Work &w, cudaStream_t st) {
+  const dim3 grid = rec_grid(s);
+  if (s.N <= 32) rec_bwd_kernel<T, 1><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+  else if (s.N <= 64) rec_bwd_kernel<T, 2><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+  else if (s.N <= 128) rec_bwd_kernel<T, 4><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+  else rec_bwd_kernel<T, 8><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+  if (s.total == 0) return cudaGetLastError();
+  const dim3 ggrid(unsigned(s.slots < (int64_t(1) << 30) ? s.slots : int64_t(1) << 30), unsigned(s.H));
+  grads_kernel<T><<<ggrid, kGThreads, 0, st>>>(s, a, sv.states, sv.es, w.dstates, w.F, w.dqh, w.dkh);
+  const int64_t want = (s.total * s.G * s.N + 255) / 256;
+  shared_kernel<T><<<unsigned(want < 8192 ? want : 8192), 256, 0, st>>>(s, w.dqh, w.dkh, static_cast<T *>(a.dq),
+                                                                        static_cast<T *>(a.dk));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t general_saved(const Shape &s) { return carve_saved(s, nullptr).bytes; }
+size_t general_bwd_workspace(const Shape &s) { return carve_work(s, nullptr).bytes; }
+
+cudaError_t general_fwd(const Shape &s, bool bf16, const Args &a, void *saved, cudaStream_t st) {
+  Saved sv{};
+  if (saved != nullptr) sv = carve_saved(s, saved);
+  return bf16 ? launch_fwd<__nv_bfloat16, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st)
+              : launch_fwd<float, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st);
+}
+
+cudaError_t general_step(const Shape &s, bool bf16, const Args &a, float *pool, const int32_t *slots, int64_t nslots,
+                         cudaStream_t st) {
+  return bf16 ? launch_fwd<__nv_bfloat16, true>(s, a, nullptr, nullptr, pool, slots, nslots, st)
+              : launch_fwd<float, true>(s, a, nullptr, nullptr, pool, slots, nslots, st);
+}
+
+cudaError_t general_bwd(const Shape &s, bool bf16, const Args &a, const void *saved, void *ws, cudaStream_t st) {
+  const Saved sv = carve_saved(s, const_cast<void *>(saved));
+  const Work w = carve_work(s, ws);
+  return bf16 ? launch_bwd<__nv_bfloat16>(s, a, sv, w, st) : launch_bwd<float>(s, a, sv, w, st);
+}
+
+}  // namespace delta
+}  // namespace ssd

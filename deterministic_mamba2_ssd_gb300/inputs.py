@@ -130,3 +130,31 @@ CONV_WORKLOADS = {
     "conv_varlen_T32768": dict(batch=1, seqlen=32768, channels=128 * 64 + 2 * 1 * 256, width=4,
                                seq_lens=(4096, 8192, 8192, 12288)),
 }
+
+
+def make_delta_inputs(b, T, H, P, G, N, dtype=torch.bfloat16, seed=0, seq_lens=(), with_init=False, with_dfinal=False):
+    """Inputs of the gated delta rule: unit-length q and k, v and dout ~ N(0,1),
+    g = A softplus(N(0,1) - 2) with A = -exp(U(log 1, log 16)) per head, beta =
+    sigmoid(N(0,1)); initial states and their gradients ~ 0.3 N(0,1).  seq_lens
+    (b must be 1): lengths of the packed sequences, zeros allowed."""
+    gen = torch.Generator().manual_seed(1234 + seed)
+
+    def rn(*shape):
+        return torch.randn(shape, generator=gen)
+
+    def unit(x):
+        return x / x.square().sum(-1, keepdim=True).add(1e-6).sqrt()
+
+    d = dict(q=unit(rn(b, T, G, N)).to(dtype), k=unit(rn(b, T, G, N)).to(dtype), v=rn(b, T, H, P).to(dtype))
+    A = -torch.exp(torch.rand(H, generator=gen) * math.log(16.0))
+    d["g"] = A * torch.nn.functional.softplus(rn(b, T, H) - 2.0)
+    d["beta"] = torch.sigmoid(rn(b, T, H))
+    d["dout"] = rn(b, T, H, P).to(dtype)
+    nseq = len(seq_lens) or b
+    d["cu"] = None
+    if seq_lens:
+        assert b == 1 and sum(seq_lens) == T
+        d["cu"] = torch.tensor([0] + list(seq_lens)).cumsum(0).to(torch.int32)
+    d["init"] = 0.3 * rn(nseq, H, P, N) if with_init else None
+    d["dfinal"] = 0.3 * rn(nseq, H, P, N) if with_dfinal else None
+    return d

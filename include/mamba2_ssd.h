@@ -393,6 +393,124 @@ ssd_status mamba2_ssd_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t channels
                                  const int32_t *seq_idx, const void *dy, float *dx, float *dweight, float *dbias,
                                  void *workspace, size_t workspace_bytes, int config, int variant, void *stream);
 
+/* ---- Norm of queries and keys, with the position rotation ---------------
+ * The step before a delta-rule scan (or any attention): per token and head,
+ * with x a row of headdim elements of q or k,
+ *     m = mean(x^2) (SSD_NORM_RMS) or sum(x^2) (SSD_NORM_L2)
+ *     y = x / sqrt(m + eps) * w          (w: wq or wk, or 1 where both are NULL)
+ * and the first `rotary` elements of y turned in pairs (a, b) = (i, i +
+ * rotary/2), or (2i, 2i+1) when interleaved, by the angle whose cosine and
+ * sine stand at row positions[token], column i of the tables:
+ *     z_a = y_a cos - y_b sin,  z_b = y_a sin + y_b cos.
+ * fp32 arithmetic, z rounded once.  q and k may be slices of a wider
+ * projection (q_stride, k_stride); z is densely packed.  Pointers need the
+ * alignment of their elements only (16-byte rows take the wide kernels).  A
+ * position outside [0, positions) turns its token's rows (and the weights'
+ * gradients) into NaN; nothing outside the tables is read. */
+typedef enum { SSD_NORM_RMS = 0, SSD_NORM_L2 = 1 } ssd_norm;
+typedef struct {
+  int64_t tokens;              /* rows of q and k; 0 launches nothing */
+  int64_t q_stride, k_stride;  /* elements between consecutive tokens; 0: packed (heads * headdim) */
+  int64_t positions;           /* rows of the cosine and sine tables (rotary > 0) */
+  int32_t qheads, kheads;      /* 1..65536 */
+  int32_t headdim;             /* 1..512 */
+  int32_t rotary;              /* even, 0..headdim */
+  int32_t interleaved;         /* 0 or 1 */
+  int32_t norm;                /* ssd_norm */
+  int32_t dtype;               /* ssd_dtype of q, k, z and their gradients */
+  float eps;                   /* >= 0, finite */
+} ssd_qk_dims;
+
+/* yq (tokens, qheads, headdim), yk (tokens, kheads, headdim).  wq, wk
+ * (headdim) fp32, both or neither; cos, sin (positions, rotary/2) fp32 and
+ * positions_of (tokens) int32, all required with rotary > 0. */
+ssd_status mamba2_ssd_qk_fwd(const ssd_qk_dims *dims, const void *q, const void *k, const float *wq, const float *wk,
+                             const float *cos, const float *sin, const int32_t *positions_of, void *yq, void *yk,
+                             void *stream);
+
+/* Workspace bytes of mamba2_ssd_qk_bwd with weights (0 for invalid dims). */
+size_t mamba2_ssd_qk_bwd_workspace_size(const ssd_qk_dims *dims);
+
+/* Backward of L = sum(yq * dyq) + sum(yk * dyk): dq, dk in dtype, densely
+ * packed; dwq, dwk (headdim) fp32, given exactly when the weights are: sums
+ * over all rows, taken in one fixed order whatever the device (a fixed number
+ * of partials, folded in a fixed order).  The forward's inputs are all it
+ * needs; the norms are computed again. */
+ssd_status mamba2_ssd_qk_bwd(const ssd_qk_dims *dims, const void *q, const void *k, const void *dyq, const void *dyk,
+                             const float *wq, const float *wk, const float *cos, const float *sin,
+                             const int32_t *positions_of, void *dq, void *dk, float *dwq, float *dwk, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* ---- Gated delta rule ---------------------------------------------------
+ * Linear attention whose state forgets by a gate and corrects itself by the
+ * delta rule.  Per row b and head h (keys and queries of group h /
+ * (nheads/ngroups)), with a state S (headdim x dstate) and per token a log
+ * decay g (<= 0 expected), a step size beta, key k, query q and value v:
+ *
+ *     S <- exp(g) S;  e = v - S k;  S <- S + beta e k^T;  o = scale S q
+ *
+ * q, k (batch, seqlen, ngroups, dstate) and v (batch, seqlen, nheads,
+ * headdim) in dtype, each possibly a slice of wider rows; g, beta (batch,
+ * seqlen, nheads) fp32; o like v, densely packed; states (.., nheads,
+ * headdim, dstate) fp32.  g of -infinity forgets everything before the token.
+ *
+ * Sequences: without SSD_DELTA_CU_SEQLENS each batch row is one (nseq =
+ * batch).  With it batch is 1 and cu_seqlens (nseq + 1 int32, device) holds
+ * each sequence's first token, from 0, never decreasing, to seqlen;
+ * sequences may be empty.  The table is read by the kernels only: a wrong one
+ * gives unspecified results but no access outside the arrays.
+ *
+ * Results are bitwise reproducible: every element has one writer and every
+ * sum one order. */
+#define SSD_DELTA_CU_SEQLENS 1
+typedef struct {
+  int64_t batch, seqlen, nheads, headdim, ngroups, dstate;   /* batch * (seqlen + 1) < 2^31; dstate <= 256 */
+  int64_t nseq;
+  int64_t q_stride, k_stride, v_stride;   /* elements between consecutive tokens; 0: packed */
+  int32_t dtype;                          /* ssd_dtype */
+  int32_t flags;                          /* SSD_DELTA_* */
+} ssd_delta_dims;
+
+/* Bytes of the forward's record for the backward, and of the workspaces (0 for invalid dims). */
+size_t mamba2_ssd_delta_saved_size(const ssd_delta_dims *dims);
+size_t mamba2_ssd_delta_fwd_workspace_size(const ssd_delta_dims *dims);
+size_t mamba2_ssd_delta_bwd_workspace_size(const ssd_delta_dims *dims);
+
+/* Name of the kernels that these dims run on (static string). */
+const char *mamba2_ssd_delta_path_name(const ssd_delta_dims *dims);
+
+/* Forward.  init_states (nseq, nheads, headdim, dstate) may be NULL (zero);
+ * final_states, likewise shaped, may be NULL (not wanted), as may `saved`
+ * (no backward will follow), else >= mamba2_ssd_delta_saved_size bytes.
+ * States, saved and workspace 16-byte aligned. */
+ssd_status mamba2_ssd_delta_fwd(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                                const float *beta, const int32_t *cu_seqlens, const float *init_states, float scale,
+                                void *o, float *final_states, void *saved, size_t saved_bytes, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* Backward of L = sum(o * dout) + sum(final_states * dfinal), from the
+ * forward's inputs and record.  dout like o; dfinal fp32 or NULL (zero).
+ * Outputs, densely packed and fully overwritten: dq, dk (batch, seqlen,
+ * ngroups, dstate; summed over the heads of a group in ascending order), dv
+ * (batch, seqlen, nheads, headdim), dg and dbeta (batch, seqlen, nheads), all
+ * in dtype; dinit fp32 or NULL (not wanted). */
+ssd_status mamba2_ssd_delta_bwd(const ssd_delta_dims *dims, const void *q, const void *k, const float *g,
+                                const float *beta, const int32_t *cu_seqlens, float scale, const void *saved,
+                                size_t saved_bytes, const void *dout, const float *dfinal, void *dq, void *dk, void *dv,
+                                void *dg, void *dbeta, float *dinit, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* Recurrent form for serving: row b (of batch = nseq) brings seqlen tokens
+ * (one, or a few drafted ones) to the state at states[slots[b]] (num_slots,
+ * nheads, headdim, dstate; fp32, 16-byte aligned), which is updated in place;
+ * o (batch, seqlen, nheads, headdim) in dtype.  slots (batch) int32 device, or
+ * NULL for slot b of row b.  A row whose slot is outside [0, num_slots) is
+ * idle: its o is zero and no state is touched.  Two rows must not share a
+ * slot. */
+ssd_status mamba2_ssd_delta_step(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                                 const float *beta, float scale, float *states, int64_t num_slots, const int32_t *slots,
+                                 void *o, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
