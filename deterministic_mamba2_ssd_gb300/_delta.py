@@ -253,10 +253,11 @@ def _delta_run(q, k, v, g, beta, scale, cu_seqlens, init_states, want_final, wan
         final = torch.empty((dims.nseq, dims.nheads, dims.headdim, dims.dstate), dtype=torch.float32,
                             device=dev) if want_final else None
         saved = torch.empty(L.mamba2_ssd_delta_saved_size(at), dtype=torch.uint8, device=dev) if want_saved else None
-        ws = torch.empty(L.mamba2_ssd_delta_fwd_workspace_size(at), dtype=torch.uint8, device=dev)
+        ws = None if want_saved else torch.empty(L.mamba2_ssd_delta_fwd_workspace_size(at), dtype=torch.uint8, device=dev)
         rc = L.mamba2_ssd_delta_fwd(at, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens),
                                     _ptr(init_states), scale, _ptr(o), _ptr(final), _ptr(saved),
-                                    0 if saved is None else saved.numel(), _ptr(ws), ws.numel(), st)
+                                    0 if saved is None else saved.numel(), _ptr(ws),
+                                    0 if ws is None else ws.numel(), st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_delta_fwd")
     keep = dict(q=q, k=k, g=g, beta=beta, cu_seqlens=cu_seqlens, init=init_states, saved=saved, final=final)

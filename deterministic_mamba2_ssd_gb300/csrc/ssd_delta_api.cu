@@ -5,6 +5,7 @@
 
 #include "mamba2_ssd.h"
 #include "ssd_delta.h"
+#include "ssd_delta_tiles.cuh"
 
 namespace {
 
@@ -70,6 +71,12 @@ bool floats_ok(std::initializer_list<const void *> ps) {
   return true;
 }
 
+// Tensor-core path: 16-bit input, whole tiles of both head sizes, and a head that one CTA of the gradient kernel holds.
+bool tiles_path(const ssd_delta_dims *d) {
+  return bf16_of(d) && (d->dstate == 64 || d->dstate == 128) && d->headdim % 16 == 0 && d->headdim <= 128 &&
+         d->nseq <= 65535;
+}
+
 ssd_status status_of(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
 }  // namespace
@@ -77,16 +84,25 @@ ssd_status status_of(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR
 extern "C" {
 
 size_t mamba2_ssd_delta_saved_size(const ssd_delta_dims *dims) {
-  return dims_ok(dims) ? ssd::delta::general_saved(shape_of(dims)) + 256 : 0;
+  if (!dims_ok(dims)) return 0;
+  const Shape s = shape_of(dims);
+  return 256 + (tiles_path(dims) ? ssd::delta::carve_tiles(s, nullptr, true).bytes : ssd::delta::general_saved(s));
 }
 
-size_t mamba2_ssd_delta_fwd_workspace_size(const ssd_delta_dims *dims) { return dims_ok(dims) ? 256 : 0; }
+size_t mamba2_ssd_delta_fwd_workspace_size(const ssd_delta_dims *dims) {
+  if (!dims_ok(dims)) return 0;
+  return 256 + (tiles_path(dims) ? ssd::delta::carve_tiles(shape_of(dims), nullptr, false).bytes : 0);
+}
 
 size_t mamba2_ssd_delta_bwd_workspace_size(const ssd_delta_dims *dims) {
-  return dims_ok(dims) ? ssd::delta::general_bwd_workspace(shape_of(dims)) + 256 : 0;
+  if (!dims_ok(dims)) return 0;
+  const Shape s = shape_of(dims);
+  return 256 + (tiles_path(dims) ? ssd::delta::carve_bwd_tiles(s, nullptr).bytes : ssd::delta::general_bwd_workspace(s));
 }
 
-const char *mamba2_ssd_delta_path_name(const ssd_delta_dims *dims) { return dims_ok(dims) ? "general" : "invalid"; }
+const char *mamba2_ssd_delta_path_name(const ssd_delta_dims *dims) {
+  return !dims_ok(dims) ? "invalid" : tiles_path(dims) ? "tiles" : "general";
+}
 
 ssd_status mamba2_ssd_delta_fwd(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
                                 const float *beta, const int32_t *cu_seqlens, const float *init_states, float scale,
@@ -100,12 +116,18 @@ ssd_status mamba2_ssd_delta_fwd(const ssd_delta_dims *dims, const void *q, const
     return SSD_ERR_INVALID_ARG;
   if (s.total > 0 && (!acts_ok(dims, {q, k, v, o}) || !floats_ok({g, beta}))) return SSD_ERR_INVALID_ARG;
   if (saved != nullptr && saved_bytes < mamba2_ssd_delta_saved_size(dims)) return SSD_ERR_WORKSPACE;
-  if (workspace_bytes < mamba2_ssd_delta_fwd_workspace_size(dims)) return SSD_ERR_WORKSPACE;
-  if (workspace == nullptr) return SSD_ERR_INVALID_ARG;
+  if (saved == nullptr) {
+    if (workspace_bytes < mamba2_ssd_delta_fwd_workspace_size(dims)) return SSD_ERR_WORKSPACE;
+    if (workspace == nullptr) return SSD_ERR_INVALID_ARG;
+  }
   Args a{};
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.cu = cu_seqlens, a.init = init_states, a.o = o;
   a.fin = final_states, a.scale = scale;
-  return status_of(ssd::delta::general_fwd(s, bf16_of(dims), a, saved, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!tiles_path(dims)) return status_of(ssd::delta::general_fwd(s, bf16_of(dims), a, saved, st));
+  const ssd::delta::Tiles t = ssd::delta::carve_tiles(s, saved != nullptr ? saved : workspace, saved != nullptr);
+  const cudaError_t e = ssd::delta::launch_prep(s, a, t, final_states != nullptr, st);
+  return status_of(e != cudaSuccess ? e : ssd::delta::launch_chain_fwd(s, a, t, st));
 }
 
 ssd_status mamba2_ssd_delta_bwd(const ssd_delta_dims *dims, const void *q, const void *k, const float *g,
@@ -127,7 +149,12 @@ ssd_status mamba2_ssd_delta_bwd(const ssd_delta_dims *dims, const void *q, const
   Args a{};
   a.q = q, a.k = k, a.g = g, a.beta = beta, a.cu = cu_seqlens, a.scale = scale, a.dout = dout, a.dfinal = dfinal;
   a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dinit = dinit;
-  return status_of(ssd::delta::general_bwd(s, bf16_of(dims), a, saved, workspace, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!tiles_path(dims)) return status_of(ssd::delta::general_bwd(s, bf16_of(dims), a, saved, workspace, st));
+  const ssd::delta::Tiles t = ssd::delta::carve_tiles(s, const_cast<void *>(saved), true);
+  const ssd::delta::BwdTiles w = ssd::delta::carve_bwd_tiles(s, workspace);
+  const cudaError_t e = ssd::delta::launch_chain_bwd(s, a, t, w, st);
+  return status_of(e != cudaSuccess ? e : ssd::delta::launch_grads(s, a, t, w, st));
 }
 
 ssd_status mamba2_ssd_delta_step(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,

@@ -1,0 +1,87 @@
+// ssd_delta_tiles.cuh -- what the tensor-core kernels of the gated delta rule
+// hand to one another: per chunk and head (or group) fp16 tiles in the
+// chunk-swizzled layout of mma16.cuh, each with the power-of-two scales that
+// keep its values inside fp16's range.
+//
+//   K16, Q16 (slot, group):  k, q of 64 tokens, rows [token][dstate], times
+//                            2^-a (2^-b): the tile's largest element in [8, 16),
+//                            so that bf16 input is exact down to 2^-21 of it
+//                            and no sum of 128 products leaves fp16's range
+//   T16 (slot, head):        (I + A)^-1, rows [t][s] times 2^-tau_t; a second
+//                            plane with the rounding left over
+//   P16 (slot, head):        exp(G_t - G_s) (q16_t . k16_s), s <= t
+//   vec (slot, head):        kVec floats, see the offsets below
+//   S16 (slot, head):        state entering the chunk, rows [p][n] times 2^-r_p
+//   E16 (slot, head):        e of the chunk, rows [t][p], column p times 2^-r_p
+//   up  (slot, head):        2^r_p
+// and from the backward chain D16, R16 and ub likewise: the gradient of the
+// state leaving the chunk and dR = beta F.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "mma16.cuh"
+#include "ssd_delta.h"
+
+namespace ssd {
+namespace delta {
+
+constexpr int kVecEg = 0;       // exp(G_t)
+constexpr int kVecTail = 64;    // exp(G_C - G_t)
+constexpr int kVecBeta = 128;
+constexpr int kVecTau = 192;    // 2^tau_t
+constexpr int kVecKa = 256;     // 2^a
+constexpr int kVecQa = 257;     // 2^b
+constexpr int kVecG = 272;      // G_t
+constexpr int kVecGl = 336;     // and what its rounding left over
+constexpr int kVec = 400;
+constexpr int kVecChain = 260;  // the part that the chains read
+constexpr int kTri = kChunk * kChunk;   // elements of a T16 or P16 plane
+
+struct Tiles {
+  __half *K16, *Q16, *T16, *P16, *S16, *E16;
+  float *vec, *up;
+  size_t bytes;
+};
+
+// record: with the parts that only a backward reads.
+inline Tiles carve_tiles(const Shape &s, void *p, bool record) {
+  Carver c(p);
+  Tiles t{};
+  t.K16 = c.take<__half>(s.slots * s.G * kChunk * s.N);
+  t.Q16 = c.take<__half>(s.slots * s.G * kChunk * s.N);
+  t.T16 = c.take<__half>(s.slots * s.H * 2 * kTri);
+  t.P16 = c.take<__half>(s.slots * s.H * kTri);
+  t.vec = c.take<float>(s.slots * s.H * kVec);
+  if (record) {
+    t.S16 = c.take<__half>(s.slots * s.H * s.P * s.N);
+    t.E16 = c.take<__half>(s.slots * s.H * kChunk * s.P);
+    t.up = c.take<float>(s.slots * s.H * s.P);
+  }
+  t.bytes = c.bytes();
+  return t;
+}
+
+struct BwdTiles {
+  __half *D16, *R16;
+  float *ub;
+  size_t bytes;
+};
+inline BwdTiles carve_bwd_tiles(const Shape &s, void *p) {
+  Carver c(p);
+  BwdTiles t{};
+  t.D16 = c.take<__half>(s.slots * s.H * s.P * s.N);
+  t.R16 = c.take<__half>(s.slots * s.H * kChunk * s.P);
+  t.ub = c.take<float>(s.slots * s.H * s.P);
+  t.bytes = c.bytes();
+  return t;
+}
+
+// Kernel launches (ssd_delta_prep.cu, ssd_delta_chain.cu, ssd_delta_grads.cu).
+cudaError_t launch_prep(const Shape &s, const Args &a, const Tiles &t, bool two_planes, cudaStream_t st);
+cudaError_t launch_chain_fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st);
+cudaError_t launch_chain_bwd(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st);
+cudaError_t launch_grads(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st);
+
+}  // namespace delta
+}  // namespace ssd

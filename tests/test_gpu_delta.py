@@ -7,7 +7,8 @@ GPU saw):
   element, and the tensor-core kernels round operands to 11 bits (2^-12 each,
   a handful in sequence): 2^-9 + 1e-3 in all, 2.95e-3;
 * fp32 states from bf16 inputs 1e-5: they are carried with operands of 22 bits
-  where they are asked for;
+  where they are asked for; dinit, a gradient that leaves unrounded, 1e-3 (the
+  operands' rounding alone);
 * dg is a sum of P x N terms of both signs: besides its own relative bar, a
   thousandth of that bar times the sum of the terms' magnitudes.
 """
@@ -58,7 +59,7 @@ def _check(d, scale=None, wide=False):
     ref = od.bwd(*(d[n] for n in NAMES), sc, d["dout"], d["init"], d["cu"], d["dfinal"])
     tol = TOL[dt]
     share = {"o": _off(o, ref["o"], tol), "final": _off(saved.final, ref["final"], STATE_TOL),
-             "dinit": _off(r["dinit"], ref["dinit"], STATE_TOL)}
+             "dinit": _off(r["dinit"], ref["dinit"], STATE_TOL if dt == torch.float32 else 1e-3)}
     for n in ("dq", "dk", "dv", "dbeta"):
         share[n] = _off(r[n], ref[n], tol)
         assert r[n].dtype == dt
