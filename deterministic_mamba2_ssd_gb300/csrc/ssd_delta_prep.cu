@@ -1,14 +1,20 @@
 // ssd_delta_prep.cu -- the part of the gated delta rule that chunks can do
-// side by side: for every chunk and head the inverse of the unit lower
-// triangular I + A (A_ts = exp(G_t - G_s) (k_t . k_s) beta_s, s < t), the
-// decayed scores q_t . k_s, and the vectors of decays and scales (see
-// ssd_delta_tiles.cuh).
+// side by side: for every chunk and head, with L_ts = exp(G_t - G_s) (k_t . k_s)
+// for s < t, the matrix Y = (I + L diag(beta))^-1 L, the decayed scores
+// q_t . k_s, and the vectors of decays and scales (see ssd_delta_tiles.cuh).
+// Y serves both directions without a division by beta:
+//     (I + L diag(beta))^-1 R = R - Y (beta R),
+//     (I + diag(beta) L)^-T U = U - Y^T (beta U).
 //
 // CTA (chunk slot, group): k and q of the chunk once, K K^T and Q K^T on the
 // tensor cores (fp16 operands are exact here: bf16 rows scaled by a power of
-// two), then the heads of the group, two at a time.  The inverse is taken in
-// fp32 by forward substitution, one thread a column with the column in
-// registers: X[t][j] = I[t][j] - sum_{s<t} A[t][s] X[s][j].
+// two), then the heads of the group, two at a time.  Y is found in fp32 by
+// forward substitution, one thread a column, 16 rows at a time:
+//     Y[t][j] = L[t][j] - sum_{j<s<t} L[t][s] beta_s Y[s][j],
+// the 16 rows as packed pairs of fp32, earlier rows of the column read back
+// from shared memory.  (With the whole column in registers the unrolled code,
+// 2000 products, did not fit the instruction cache: 220 us instead of 80 for
+// 256 chunks of 32 heads.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,9 +31,16 @@ constexpr int kPad = kChunk + 4;   // floats of a row of A and X in shared memor
 
 template <int N>
 struct Smem {
-  __half k[kChunk * N], q[kChunk * N];
-  float A[2][kChunk][kPad];        // A of two heads; then X in its place
-  float top[2][kThreads / 32];     // largest |k|, |q| of each warp's part
+  union {
+    struct {
+      __half k[kChunk * N], q[kChunk * N];
+    };
+    struct {   // of two heads, once the products of k and q are taken
+      float L[2][kChunk][kPad];   // [s][t]
+      float Y[2][kChunk][kPad];   // [t][s]
+    };
+  };
+  float top[2][kThreads / 32];    // largest |k|, |q| of each warp's part
   float G[2][kChunk], Gl[2][kChunk], beta[2][kChunk];
 };
 
@@ -88,21 +101,49 @@ __device__ __forceinline__ void rows_out(const uint4 (&raw)[kChunk * N / 8 / kTh
   }
 }
 
-// Rows t0..63 of column j of X by forward substitution; rows before t0 (and the column's rows above j) are zero.
-template <int t0>
-__device__ __forceinline__ void substitute(const float (*A)[kPad], int j, float (&x)[kChunk]) {
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b),
+                     z = *reinterpret_cast<unsigned long long *>(&c);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(z) : "l"(x), "l"(y));
+  return *reinterpret_cast<float2 *>(&z);
+}
+
+// Column j of Y; a warp has 32 neighbouring columns, the first of them j0 (rows up to j0 are zero).
+__device__ __forceinline__ void solve(const float (*L)[kPad], const float *beta, float (*Y)[kPad], int j, int j0) {
+#pragma unroll 1
+  for (int r0 = j0; r0 < kChunk; r0 += 16) {
+    float2 acc[8];
+    const bool below = r0 + 16 > j;   // this strip of rows has a part of L's column j
 #pragma unroll
-  for (int t = t0; t < kChunk; ++t) {
-    float acc[4] = {t == j ? 1.f : 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = t0; s < t; s += 4) {
-      const float4 a = *reinterpret_cast<const float4 *>(&A[t][s]);
-      acc[0] = fmaf(-a.x, x[s], acc[0]);
-      if (s + 1 < t) acc[1] = fmaf(-a.y, x[s + 1], acc[1]);
-      if (s + 2 < t) acc[2] = fmaf(-a.z, x[s + 2], acc[2]);
-      if (s + 3 < t) acc[3] = fmaf(-a.w, x[s + 3], acc[3]);
+    for (int i = 0; i < 8; i += 2) {
+      const float4 v = below ? *reinterpret_cast<const float4 *>(&L[j][r0 + 2 * i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      acc[i] = make_float2(v.x, v.y);
+      acc[i + 1] = make_float2(v.z, v.w);
     }
-    x[t] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll 4
+    for (int s = j0; s < r0; ++s) {
+      const float z = -beta[s] * Y[s][j];
+      const float2 zz = make_float2(z, z);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float4 v = *reinterpret_cast<const float4 *>(&L[s][r0 + 2 * i]);
+        acc[i] = fma2(make_float2(v.x, v.y), zz, acc[i]);
+        acc[i + 1] = fma2(make_float2(v.z, v.w), zz, acc[i + 1]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const float y = t & 1 ? acc[t >> 1].y : acc[t >> 1].x;
+      Y[r0 + t][j] = y;
+      const float z = -beta[r0 + t] * y;
+      const float2 zz = make_float2(z, z);
+#pragma unroll
+      for (int i = (t + 1) / 4 * 2; i < 8; i += 2) {   // L is zero on and above the diagonal of this block
+        const float4 v = *reinterpret_cast<const float4 *>(&L[r0 + t][r0 + 2 * i]);
+        acc[i] = fma2(make_float2(v.x, v.y), zz, acc[i]);
+        acc[i + 1] = fma2(make_float2(v.z, v.w), zz, acc[i + 1]);
+      }
+    }
   }
 }
 
@@ -130,9 +171,10 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
     top[0] = fmaxf(top[0], sm.top[0][i]);
     top[1] = fmaxf(top[1], sm.top[1][i]);
   }
-  const float ka = pow2_above(top[0] * 0.0625f), qa = pow2_above(top[1] * 0.0625f);
+  // one scale for both, so that their products with one matrix can be added up
+  const float ka = pow2_above(fmaxf(top[0], top[1]) * 0.0625f);
   rows_out<N>(rk, pow2_inv(ka), sm.k, o.K16 + tile);
-  rows_out<N>(rq, pow2_inv(qa), sm.q, o.Q16 + tile);
+  rows_out<N>(rq, pow2_inv(ka), sm.q, o.Q16 + tile);
   __syncthreads();
   // rows 16 warp.. of K K^T and Q K^T, columns up to the diagonal block
   float kk[8][4] = {}, qk[8][4] = {};
@@ -156,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
   const int rows[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};
   for (int h0 = 0; h0 < s.hpg; h0 += 2) {
     const int nh = min(2, s.hpg - h0);
-    __syncthreads();   // the heads before are done with A and the vectors
+    __syncthreads();   // the products of k and q are taken, the heads before are done with L, Y and the vectors
     // running sums of g as hi + lo by a scan over 32 lanes x 2 tokens, warp w < 2 for head w
     if (warp < nh) {
       const int h = grp * s.hpg + h0 + warp;
@@ -196,23 +238,21 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
       uint8_t *P = reinterpret_cast<uint8_t *>(o.P16 + at * kTri);
       const float Gr[2] = {G[rows[0]], G[rows[1]]}, Glr[2] = {Gl[rows[0]], Gl[rows[1]]};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = 8 * j + 2 * (lane & 3);
-        const float g0 = G[c], g1 = G[c + 1], l0 = Gl[c], l1 = Gl[c + 1];
-        const float w0 = sm.beta[w][c] * ka * ka, w1 = sm.beta[w][c + 1] * ka * ka;
+      for (int j = 0; j < 8; ++j)
+        if (j <= 2 * warp + 1) {   // blocks above the diagonal are never read
+          const int c = 8 * j + 2 * (lane & 3);
+          const float g0 = G[c], g1 = G[c + 1], l0 = Gl[c], l1 = Gl[c + 1];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = rows[i];
-          const float d0 = c <= t ? __expf(acs_diff(Gr[i], Glr[i], g0, l0)) : 0.f;
-          const float d1 = c + 1 <= t ? __expf(acs_diff(Gr[i], Glr[i], g1, l1)) : 0.f;
-          float2 av;
-          av.x = c < t ? d0 * kk[j][2 * i] * w0 : 0.f;
-          av.y = c + 1 < t ? d1 * kk[j][2 * i + 1] * w1 : 0.f;
-          *reinterpret_cast<float2 *>(&sm.A[w][t][c]) = av;
-          *reinterpret_cast<uint32_t *>(P + swz(t, j, 128) + 4 * (lane & 3)) =
-              pack(d0 * qk[j][2 * i], d1 * qk[j][2 * i + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const int t = rows[i];
+            const float d0 = c <= t ? __expf(acs_diff(Gr[i], Glr[i], g0, l0)) : 0.f;
+            const float d1 = c + 1 <= t ? __expf(acs_diff(Gr[i], Glr[i], g1, l1)) : 0.f;
+            sm.L[w][c][t] = c < t ? d0 * kk[j][2 * i] * (ka * ka) : 0.f;
+            sm.L[w][c + 1][t] = c + 1 < t ? d1 * kk[j][2 * i + 1] * (ka * ka) : 0.f;
+            *reinterpret_cast<uint32_t *>(P + swz(t, j, 128) + 4 * (lane & 3)) =
+                pack(d0 * qk[j][2 * i], d1 * qk[j][2 * i + 1]);
+          }
         }
-      }
       if (tid < kChunk) {
         float *v = o.vec + at * kVec;
         v[kVecEg + tid] = expf(G[tid] + Gl[tid]);
@@ -220,38 +260,23 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
         v[kVecBeta + tid] = sm.beta[w][tid];
         v[kVecG + tid] = G[tid];
         v[kVecGl + tid] = Gl[tid];
-        if (tid < 2) v[kVecKa + tid] = tid == 0 ? ka : qa;
+        if (tid == 0) v[kVecKa] = ka;
       }
     }
     __syncthreads();
-    {
-      const int w = warp >> 1, j = tid & 63;
-      float x[kChunk];
-      if (w < nh) {
-        if (j < 32) {
-          substitute<0>(sm.A[w], j, x);
-        } else {
-#pragma unroll
-          for (int t = 0; t < 32; ++t) x[t] = 0.f;
-          substitute<32>(sm.A[w], j, x);
-        }
-      }
-      __syncthreads();
-      if (w < nh) {
-#pragma unroll
-        for (int t = 0; t < kChunk; ++t) sm.A[w][t][j] = x[t];
-      }
-    }
+    if ((warp >> 1) < nh) solve(sm.L[warp >> 1], sm.beta[warp >> 1], sm.Y[warp >> 1], tid & 63, 32 * (warp & 1));
     __syncthreads();
-    // rows of X to fp16, eight lanes a row
+    // rows of Y to fp16, eight lanes a row
     for (int w = 0; w < nh; ++w) {
       const int64_t at = slot * s.H + grp * s.hpg + h0 + w;
-      uint8_t *T = reinterpret_cast<uint8_t *>(o.T16 + at * 2 * kTri);
+      uint8_t *Y = reinterpret_cast<uint8_t *>(o.Y16 + at * 2 * kTri);
 #pragma unroll 2
       for (int r = tid / 8; r < kChunk; r += kThreads / 8) {
         const int l = tid % 8;
-        const float4 u0 = *reinterpret_cast<const float4 *>(&sm.A[w][r][8 * l]);
-        const float4 u1 = *reinterpret_cast<const float4 *>(&sm.A[w][r][8 * l + 4]);
+        // columns from 32 have no rows above 32
+        const bool on = l < 4 || r >= 32;
+        const float4 u0 = on ? *reinterpret_cast<const float4 *>(&sm.Y[w][r][8 * l]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 u1 = on ? *reinterpret_cast<const float4 *>(&sm.Y[w][r][8 * l + 4]) : make_float4(0.f, 0.f, 0.f, 0.f);
         const float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
         float m = 0.f;
 #pragma unroll
@@ -267,9 +292,9 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
           hi[i] = p[0];
           lo[i] = p[1];
         }
-        *reinterpret_cast<uint4 *>(T + swz(r, l, 128)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(Y + swz(r, l, 128)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         if (two_planes)
-          *reinterpret_cast<uint4 *>(T + 2 * kTri + swz(r, l, 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4 *>(Y + 2 * kTri + swz(r, l, 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (l == 0) o.vec[at * kVec + kVecTau + r] = sc;
       }
     }

@@ -4,18 +4,20 @@
 // keep its values inside fp16's range.
 //
 //   K16, Q16 (slot, group):  k, q of 64 tokens, rows [token][dstate], times
-//                            2^-a (2^-b): the tile's largest element in [8, 16),
+//                            2^-a: the larger tile's largest element in [8, 16),
 //                            so that bf16 input is exact down to 2^-21 of it
 //                            and no sum of 128 products leaves fp16's range
-//   T16 (slot, head):        (I + A)^-1, rows [t][s] times 2^-tau_t; a second
-//                            plane with the rounding left over
+//   Y16 (slot, head):        (I + L diag(beta))^-1 L, rows [t][s] times
+//                            2^-tau_t; a second plane with the rounding left over
 //   P16 (slot, head):        exp(G_t - G_s) (q16_t . k16_s), s <= t
+//                            (16 x 16 blocks above the diagonal not written)
 //   vec (slot, head):        kVec floats, see the offsets below
-//   S16 (slot, head):        state entering the chunk, rows [p][n] times 2^-r_p
-//   E16 (slot, head):        e of the chunk, rows [t][p], column p times 2^-r_p
-//   up  (slot, head):        2^r_p
-// and from the backward chain D16, R16 and ub likewise: the gradient of the
-// state leaving the chunk and dR = beta F.
+//   S16 (slot, head):        state entering the chunk, rows [p][n] times 2^-r
+//   E16 (slot, head):        e of the chunk, rows [t][p] (not swizzled) times 2^-r
+//   up  (slot, head):        2^r, one for each strip of 16 p
+// and from the backward chain, with scales ub of its own: D16 like S16, the
+// gradient of the state leaving the chunk; F16 and X16 like E16, F = dS k and
+// dout.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -31,15 +33,14 @@ constexpr int kVecTail = 64;    // exp(G_C - G_t)
 constexpr int kVecBeta = 128;
 constexpr int kVecTau = 192;    // 2^tau_t
 constexpr int kVecKa = 256;     // 2^a
-constexpr int kVecQa = 257;     // 2^b
 constexpr int kVecG = 272;      // G_t
 constexpr int kVecGl = 336;     // and what its rounding left over
 constexpr int kVec = 400;
 constexpr int kVecChain = 260;  // the part that the chains read
-constexpr int kTri = kChunk * kChunk;   // elements of a T16 or P16 plane
+constexpr int kTri = kChunk * kChunk;   // elements of a Y16 or P16 plane
 
 struct Tiles {
-  __half *K16, *Q16, *T16, *P16, *S16, *E16;
+  __half *K16, *Q16, *Y16, *P16, *S16, *E16;
   float *vec, *up;
   size_t bytes;
 };
@@ -50,20 +51,20 @@ inline Tiles carve_tiles(const Shape &s, void *p, bool record) {
   Tiles t{};
   t.K16 = c.take<__half>(s.slots * s.G * kChunk * s.N);
   t.Q16 = c.take<__half>(s.slots * s.G * kChunk * s.N);
-  t.T16 = c.take<__half>(s.slots * s.H * 2 * kTri);
+  t.Y16 = c.take<__half>(s.slots * s.H * 2 * kTri);
   t.P16 = c.take<__half>(s.slots * s.H * kTri);
   t.vec = c.take<float>(s.slots * s.H * kVec);
   if (record) {
     t.S16 = c.take<__half>(s.slots * s.H * s.P * s.N);
     t.E16 = c.take<__half>(s.slots * s.H * kChunk * s.P);
-    t.up = c.take<float>(s.slots * s.H * s.P);
+    t.up = c.take<float>(s.slots * s.H * s.P / 16);
   }
   t.bytes = c.bytes();
   return t;
 }
 
 struct BwdTiles {
-  __half *D16, *R16;
+  __half *D16, *F16, *X16;
   float *ub;
   size_t bytes;
 };
@@ -71,8 +72,9 @@ inline BwdTiles carve_bwd_tiles(const Shape &s, void *p) {
   Carver c(p);
   BwdTiles t{};
   t.D16 = c.take<__half>(s.slots * s.H * s.P * s.N);
-  t.R16 = c.take<__half>(s.slots * s.H * kChunk * s.P);
-  t.ub = c.take<float>(s.slots * s.H * s.P);
+  t.F16 = c.take<__half>(s.slots * s.H * kChunk * s.P);
+  t.X16 = c.take<__half>(s.slots * s.H * kChunk * s.P);
+  t.ub = c.take<float>(s.slots * s.H * s.P / 16);
   t.bytes = c.bytes();
   return t;
 }
