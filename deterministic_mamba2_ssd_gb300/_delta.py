@@ -14,7 +14,7 @@ import functools
 
 import torch
 
-from . import SSD_BF16, SSD_F32, SsdError, _check, _ptr, lib
+from . import SSD_BF16, SSD_F32, SsdError, _check, lib
 
 DELTA_CU_SEQLENS = 1
 NORMS = {"rms": 0, "l2": 1}
@@ -64,22 +64,57 @@ def make_delta_dims(batch, seqlen, nheads, headdim, ngroups, dstate, nseq=None, 
                      k_stride, v_stride, _TYPES[dtype], DELTA_CU_SEQLENS if cu_seqlens else 0)
 
 
-# dims by their values: the sizes of a program's calls are few, and a struct of ten fields costs a few microseconds
-_qk_dims = functools.lru_cache(maxsize=256)(make_qk_dims)
-_delta_dims = functools.lru_cache(maxsize=256)(make_delta_dims)
-
-
 def delta_path_name(dims: DeltaDims) -> str:
     """Name of the kernels that these dims run on."""
     return lib().mamba2_ssd_delta_path_name(ctypes.byref(dims)).decode()
 
 
-def _scope(t, stream):
-    """(context, stream handle) in which a call on t's device allocates and launches."""
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    s = torch.cuda.current_stream(t.device) if stream is None else stream
-    return torch.cuda.stream(s), ctypes.c_void_p(s.cuda_stream)
+def _scope(device, stream):
+    """(context, stream handle) in which a call on `device` allocates and launches."""
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+        if device.index == torch.cuda.current_device():
+            return _HERE, s.cuda_stream
+        return torch.cuda.stream(s), s.cuda_stream
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+# What the checks of arguments look at.  A call's checks, struct and sizes depend on nothing else, so they are made once
+# for each set of layouts (a program has few) and found again by it: together they cost more than a small launch.
+def _layout(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+class _Like:
+    """The layout of a tensor, with the parts of its interface that the checks use."""
+
+    def __init__(self, layout):
+        self.shape, self.strides, self.dtype, self.device = layout
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return self.strides
+
+    def is_contiguous(self):
+        want = 1
+        for n, st in zip(reversed(self.shape), reversed(self.strides)):
+            if n != 1 and st != want:
+                return 0 in self.shape
+            want *= n
+        return True
+
+
+def _like(*layouts):
+    return [None if x is None else _Like(x) for x in layouts]
 
 
 def _rows(t, name, b, T, dtype, device):
@@ -110,7 +145,12 @@ def _type(t):
 
 # ---- norm of queries and keys, with rotation --------------------------------
 
-def _qk_args(q, k, wq, wk, cos, sin, positions, norm, eps, interleaved):
+@functools.lru_cache(maxsize=256)
+def _qk_plan(q, k, wq, wk, cos, sin, positions, dyq, dyk, norm, eps, interleaved):
+    """(dims, reference to it, workspace bytes of the backward) of checked layouts."""
+    if q is None or k is None:
+        raise ValueError("q and k are required")
+    q, k, wq, wk, cos, sin, positions, dyq, dyk = _like(q, k, wq, wk, cos, sin, positions, dyq, dyk)
     dt, dev = _type(q), q.device
     if q.dim() != 4:
         raise ValueError("q must be (batch, seqlen, heads, headdim)")
@@ -136,7 +176,12 @@ def _qk_args(q, k, wq, wk, cos, sin, positions, norm, eps, interleaved):
         _check(positions, "positions", (b, T), torch.int32, dev)
     elif sin is not None or positions is not None:
         raise ValueError("cos, sin and positions are given together or not at all")
-    return _qk_dims(b * T, hq, hk, d, rotary, npos, norm, dt, float(eps), bool(interleaved), qs, ks)
+    if dyq is not None:
+        _check(dyq, "dyq", tuple(q.shape), dt, dev)
+        _check(dyk, "dyk", tuple(k.shape), dt, dev)
+    dims = make_qk_dims(b * T, hq, hk, d, rotary, npos, norm, dt, float(eps), bool(interleaved), qs, ks)
+    at = ctypes.byref(dims)
+    return dims, at, lib().mamba2_ssd_qk_bwd_workspace_size(at)
 
 
 def qk_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, norm="l2", eps=1e-6, interleaved=False,
@@ -146,13 +191,14 @@ def qk_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, norm="l2"
     wk (D, fp32) if given, its first 2 * cos.shape[1] elements turned by the
     angle of the token's position (int32 (b,T) into the fp32 tables cos, sin).
     q and k may be slices of one projection; outputs are packed."""
-    dims = _qk_args(q, k, wq, wk, cos, sin, positions, norm, eps, interleaved)
-    ctx, st = _scope(q, stream)
+    at = _qk_plan(_layout(q), _layout(k), _layout(wq), _layout(wk), _layout(cos), _layout(sin), _layout(positions),
+                  None, None, norm, eps, interleaved)[1]
+    ctx, st = _scope(q.device, stream)
     with ctx:
-        yq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        yk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        rc = lib().mamba2_ssd_qk_fwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin),
-                                     _ptr(positions), _ptr(yq), _ptr(yk), st)
+        yq = q.new_empty(q.shape)
+        yk = k.new_empty(k.shape)
+        rc = lib().mamba2_ssd_qk_fwd(at, q.data_ptr(), k.data_ptr(), _at(wq), _at(wk), _at(cos), _at(sin),
+                                     _at(positions), yq.data_ptr(), yk.data_ptr(), st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_qk_fwd")
     return yq, yk
@@ -161,21 +207,21 @@ def qk_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, norm="l2"
 def qk_bwd(q, k, dyq, dyk, wq=None, wk=None, cos=None, sin=None, positions=None, norm="l2", eps=1e-6,
            interleaved=False, stream=None):
     """dict of dq, dk (in q's dtype, packed) and, with weights, dwq, dwk (fp32) of sum(yq * dyq) + sum(yk * dyk)."""
-    dims = _qk_args(q, k, wq, wk, cos, sin, positions, norm, eps, interleaved)
+    if dyq is None or dyk is None:
+        raise ValueError("dyq and dyk are required")
+    _, at, need = _qk_plan(_layout(q), _layout(k), _layout(wq), _layout(wk), _layout(cos), _layout(sin),
+                           _layout(positions), _layout(dyq), _layout(dyk), norm, eps, interleaved)
     dt, dev = q.dtype, q.device
-    _check(dyq, "dyq", tuple(q.shape), dt, dev)
-    _check(dyk, "dyk", tuple(k.shape), dt, dev)
-    ctx, st = _scope(q, stream)
+    ctx, st = _scope(dev, stream)
     with ctx:
-        out = dict(dq=torch.empty(q.shape, dtype=dt, device=dev), dk=torch.empty(k.shape, dtype=dt, device=dev))
+        out = dict(dq=q.new_empty(q.shape), dk=k.new_empty(k.shape))
         ws = None
         if wq is not None:
             out["dwq"], out["dwk"] = torch.empty_like(wq), torch.empty_like(wk)
-            ws = torch.empty(lib().mamba2_ssd_qk_bwd_workspace_size(ctypes.byref(dims)), dtype=torch.uint8, device=dev)
-        rc = lib().mamba2_ssd_qk_bwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(dyq), _ptr(dyk), _ptr(wq), _ptr(wk),
-                                     _ptr(cos), _ptr(sin), _ptr(positions), _ptr(out["dq"]), _ptr(out["dk"]),
-                                     _ptr(out.get("dwq")), _ptr(out.get("dwk")), _ptr(ws),
-                                     0 if ws is None else ws.numel(), st)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = lib().mamba2_ssd_qk_bwd(at, q.data_ptr(), k.data_ptr(), dyq.data_ptr(), dyk.data_ptr(), _at(wq), _at(wk),
+                                     _at(cos), _at(sin), _at(positions), out["dq"].data_ptr(), out["dk"].data_ptr(),
+                                     _at(out.get("dwq")), _at(out.get("dwk")), _at(ws), 0 if ws is None else need, st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_qk_bwd")
     return out
@@ -207,8 +253,9 @@ def qk_norm(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, norm="l2
 class DeltaSaved:
     """What delta_bwd needs: the forward's inputs and its record."""
 
-    def __init__(self, dims, tensors, scale):
-        self.dims = dims
+    def __init__(self, plan, tensors, scale):
+        self.plan = plan
+        self.dims = plan[0]
         self.tensors = tensors
         self.scale = scale
 
@@ -218,7 +265,12 @@ class DeltaSaved:
         return self.tensors["final"]
 
 
-def _delta_args(q, k, v, g, beta, cu_seqlens, init_states):
+@functools.lru_cache(maxsize=256)
+def _delta_plan(q, k, v, g, beta, cu_seqlens, init_states):
+    """(dims, reference to it, bytes of the record, of the forward's workspace, of the backward's) of checked layouts."""
+    if q is None or k is None or v is None:
+        raise ValueError("q, k and v are required")
+    q, k, v, g, beta, cu_seqlens, init_states = _like(q, k, v, g, beta, cu_seqlens, init_states)
     dt, dev = _type(q), q.device
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k (batch, seqlen, groups, dstate) and v (batch, seqlen, heads, headdim) are 4-dimensional")
@@ -240,28 +292,32 @@ def _delta_args(q, k, v, g, beta, cu_seqlens, init_states):
         _check(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, dev)
     if init_states is not None:
         _check(init_states, "init_states", (nseq, H, P, N), torch.float32, dev)
-    return _delta_dims(b, T, H, P, G, N, nseq, dt, cu_seqlens is not None, qs, ks, vs)
+    dims = make_delta_dims(b, T, H, P, G, N, nseq, dt, cu_seqlens is not None, qs, ks, vs)
+    at, L = ctypes.byref(dims), lib()
+    return (dims, at, L.mamba2_ssd_delta_saved_size(at), L.mamba2_ssd_delta_fwd_workspace_size(at),
+            L.mamba2_ssd_delta_bwd_workspace_size(at))
 
 
 def _delta_run(q, k, v, g, beta, scale, cu_seqlens, init_states, want_final, want_saved, stream):
-    dims = _delta_args(q, k, v, g, beta, cu_seqlens, init_states)
+    plan = _delta_plan(_layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(cu_seqlens),
+                       _layout(init_states))
+    dims, at, saved_bytes, ws_bytes, _ = plan
     scale = dims.dstate ** -0.5 if scale is None else float(scale)
-    dev, L, at = q.device, lib(), ctypes.byref(dims)
-    ctx, st = _scope(q, stream)
+    dev = q.device
+    ctx, st = _scope(dev, stream)
     with ctx:
-        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        o = v.new_empty(v.shape)
         final = torch.empty((dims.nseq, dims.nheads, dims.headdim, dims.dstate), dtype=torch.float32,
                             device=dev) if want_final else None
-        saved = torch.empty(L.mamba2_ssd_delta_saved_size(at), dtype=torch.uint8, device=dev) if want_saved else None
-        ws = None if want_saved else torch.empty(L.mamba2_ssd_delta_fwd_workspace_size(at), dtype=torch.uint8, device=dev)
-        rc = L.mamba2_ssd_delta_fwd(at, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens),
-                                    _ptr(init_states), scale, _ptr(o), _ptr(final), _ptr(saved),
-                                    0 if saved is None else saved.numel(), _ptr(ws),
-                                    0 if ws is None else ws.numel(), st)
+        saved = torch.empty(saved_bytes, dtype=torch.uint8, device=dev) if want_saved else None
+        ws = None if want_saved else torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        rc = lib().mamba2_ssd_delta_fwd(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                        _at(cu_seqlens), _at(init_states), scale, o.data_ptr(), _at(final), _at(saved),
+                                        saved_bytes if want_saved else 0, _at(ws), 0 if want_saved else ws_bytes, st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_delta_fwd")
     keep = dict(q=q, k=k, g=g, beta=beta, cu_seqlens=cu_seqlens, init=init_states, saved=saved, final=final)
-    return o, final, DeltaSaved(dims, keep, scale)
+    return o, final, DeltaSaved(plan, keep, scale)
 
 
 def delta_fwd(q, k, v, g, beta, scale=None, init_states=None, cu_seqlens=None, want_final=False, stream=None):
@@ -292,22 +348,36 @@ def delta_bwd(saved: DeltaSaved, dout, dfinal=None, want_dinit=None, stream=None
         _check(dfinal, "dfinal", states, torch.float32, dev)
     if want_dinit is None:
         want_dinit = t["init"] is not None
-    L, at = lib(), ctypes.byref(d)
-    ctx, st = _scope(q, stream)
+    _, at, saved_bytes, _, need = saved.plan
+    ctx, st = _scope(dev, stream)
     with ctx:
-        out = dict(dq=torch.empty(q.shape, dtype=dt, device=dev), dk=torch.empty(k.shape, dtype=dt, device=dev),
+        out = dict(dq=q.new_empty(q.shape), dk=k.new_empty(k.shape),
                    dv=torch.empty(shape, dtype=dt, device=dev), dg=torch.empty(shape[:3], dtype=dt, device=dev),
                    dbeta=torch.empty(shape[:3], dtype=dt, device=dev))
         if want_dinit:
             out["dinit"] = torch.empty(states, dtype=torch.float32, device=dev)
-        ws = torch.empty(L.mamba2_ssd_delta_bwd_workspace_size(at), dtype=torch.uint8, device=dev)
-        rc = L.mamba2_ssd_delta_bwd(at, _ptr(q), _ptr(k), _ptr(t["g"]), _ptr(t["beta"]), _ptr(t["cu_seqlens"]),
-                                    saved.scale, _ptr(t["saved"]), t["saved"].numel(), _ptr(dout), _ptr(dfinal),
-                                    _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]),
-                                    _ptr(out["dbeta"]), _ptr(out.get("dinit")), _ptr(ws), ws.numel(), st)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = lib().mamba2_ssd_delta_bwd(at, q.data_ptr(), k.data_ptr(), t["g"].data_ptr(), t["beta"].data_ptr(),
+                                        _at(t["cu_seqlens"]), saved.scale, t["saved"].data_ptr(), saved_bytes,
+                                        dout.data_ptr(), _at(dfinal), out["dq"].data_ptr(), out["dk"].data_ptr(),
+                                        out["dv"].data_ptr(), out["dg"].data_ptr(), out["dbeta"].data_ptr(),
+                                        _at(out.get("dinit")), ws.data_ptr(), need, st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_delta_bwd")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _step_plan(q, k, v, g, beta, states, slots):
+    dims, at = _delta_plan(q, k, v, g, beta, None, None)[:2]
+    q, states, slots = _like(q, states, slots)
+    n = states.shape[0] if states.dim() == 4 else 0
+    _check(states, "states", (n, dims.nheads, dims.headdim, dims.dstate), torch.float32, q.device)
+    if slots is not None:
+        _check(slots, "slots", (dims.batch,), torch.int32, q.device)
+    elif n < dims.batch:
+        raise ValueError("fewer states than rows")
+    return dims, at
 
 
 def delta_step(q, k, v, g, beta, states, slots=None, scale=None, stream=None):
@@ -315,19 +385,13 @@ def delta_step(q, k, v, g, beta, states, slots=None, scale=None, stream=None):
     each of b sequences, whose states (slots,H,P,N) fp32 are updated in place.
     Row i uses states[slots[i]] (slots int32; row i itself without); a slot
     outside the pool marks an idle row (o zero).  Shapes as in delta_fwd."""
-    dims = _delta_args(q, k, v, g, beta, None, None)
-    n = states.shape[0] if states.dim() == 4 else 0
-    _check(states, "states", (n, dims.nheads, dims.headdim, dims.dstate), torch.float32, q.device)
-    if slots is not None:
-        _check(slots, "slots", (dims.batch,), torch.int32, q.device)
-    elif n < dims.batch:
-        raise ValueError("fewer states than rows")
+    dims, at = _step_plan(_layout(q), _layout(k), _layout(v), _layout(g), _layout(beta), _layout(states), _layout(slots))
     scale = dims.dstate ** -0.5 if scale is None else float(scale)
-    ctx, st = _scope(q, stream)
+    ctx, st = _scope(q.device, stream)
     with ctx:
-        o = torch.empty(v.shape, dtype=v.dtype, device=q.device)
-        rc = lib().mamba2_ssd_delta_step(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), scale,
-                                         _ptr(states), n, _ptr(slots), _ptr(o), st)
+        o = v.new_empty(v.shape)
+        rc = lib().mamba2_ssd_delta_step(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                         scale, states.data_ptr(), states.shape[0], _at(slots), o.data_ptr(), st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_delta_step")
     return o

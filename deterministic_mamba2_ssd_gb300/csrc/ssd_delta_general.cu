@@ -19,7 +19,7 @@ namespace delta {
 namespace {
 
 constexpr int kRows = 16;      // state rows of a CTA
-constexpr int kBlock = 8;      // tokens staged in shared memory at a time
+constexpr int kBlock = 8;      // tokens staged in shared memory at a time; 1 or 4 where a step brings no more
 constexpr int kThreads = 128;
 
 template <class T>
@@ -71,11 +71,12 @@ __device__ __forceinline__ void store_row(const float (&s)[4 * NJ], float *row, 
 
 // One block of tokens on its way to shared memory: first every load into
 // registers (while the block before is being worked on), then the stores.
-template <class T, int NJ, bool kBwd>
+template <class T, int NJ, int TB, int RS, bool kBwd>
 struct Stage {
-  static constexpr int kWide = 32 * NJ;                       // padded dstate
-  static constexpr int kVec = kBlock * kWide / kThreads;      // q (and k) elements of a thread
-  float q[kVec], k[kVec], v, d, g, b;
+  static constexpr int kWide = 32 * NJ;                                    // padded dstate
+  static constexpr int kVec = (TB * kWide + kThreads - 1) / kThreads;      // q (and k) elements of a thread
+  static constexpr int kIn = (TB * kRows * RS + kThreads - 1) / kThreads;  // v or dout elements of a thread
+  float q[kVec], k[kVec], x[kIn], g, b;
 
   __device__ __forceinline__ void load(const Shape &s, const Args &a, int64_t t0, int64_t e, int h, int p0) {
     const int grp = h / s.hpg;
@@ -84,55 +85,66 @@ struct Stage {
     for (int i = 0; i < kVec; ++i) {
       const int x = threadIdx.x + i * kThreads, c = x % kWide;
       const int64_t t = t0 + x / kWide;
-      const bool in = t < e && c < s.N;
+      const bool in = x < TB * kWide && t < e && c < s.N;
       q[i] = in ? ld(qp + t * s.qs + c) : 0.f;
       k[i] = in ? ld(kp + t * s.ks + c) : 0.f;
     }
-    const int64_t t = t0 + threadIdx.x / kRows;
-    const int p = p0 + threadIdx.x % kRows;
-    const bool in = t < e && p < s.P;
-    if (!kBwd) v = in ? ld(static_cast<const T *>(a.v) + t * s.vs + int64_t(h) * s.P + p) : 0.f;
-    if (kBwd) d = in ? ld(static_cast<const T *>(a.dout) + (t * s.H + h) * s.P + p) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) {
+      const int y = threadIdx.x + i * kThreads, p = p0 + y % (kRows * RS);
+      const int64_t t = t0 + y / (kRows * RS);
+      const bool in = y < TB * kRows * RS && t < e && p < s.P;
+      if (kBwd) x[i] = in ? ld(static_cast<const T *>(a.dout) + (t * s.H + h) * s.P + p) : 0.f;
+      else x[i] = in ? ld(static_cast<const T *>(a.v) + t * s.vs + int64_t(h) * s.P + p) : 0.f;
+    }
     const int64_t tg = t0 + threadIdx.x;
-    const bool ing = threadIdx.x < kBlock && tg < e;
+    const bool ing = threadIdx.x < TB && tg < e;
     g = ing ? expf(a.g[tg * s.H + h]) : 1.f;    // a token past the end leaves the state as it is
     b = ing ? a.beta[tg * s.H + h] : 0.f;
   }
 };
 
-template <int NJ>
+template <int NJ, int TB, int RS>
 struct Tile {
-  float q[kBlock][32 * NJ], k[kBlock][32 * NJ];
-  float x[kBlock][kRows];      // v (forward) or dout (backward)
-  float y[kBlock][kRows];      // o (forward) or F (backward)
-  float z[kBlock][kRows];      // e (forward)
-  float g[kBlock], b[kBlock];
+  float q[TB][32 * NJ], k[TB][32 * NJ];
+  float x[TB][kRows * RS];      // v (forward) or dout (backward)
+  float y[TB][kRows * RS][8];   // each lane's part of o (forward); F at [..][0] (backward)
+  float z[TB][kRows * RS];      // e (forward)
+  float g[TB], b[TB];
 
   template <class T, bool kBwd>
-  __device__ __forceinline__ void put(const Stage<T, NJ, kBwd> &st) {
+  __device__ __forceinline__ void put(const Stage<T, NJ, TB, RS, kBwd> &st) {
 #pragma unroll
-    for (int i = 0; i < Stage<T, NJ, kBwd>::kVec; ++i) {
+    for (int i = 0; i < Stage<T, NJ, TB, RS, kBwd>::kVec; ++i) {
       const int e = threadIdx.x + i * kThreads;
-      (&q[0][0])[e] = st.q[i];
-      (&k[0][0])[e] = st.k[i];
+      if (TB * 32 * NJ % kThreads == 0 || e < TB * 32 * NJ) {
+        (&q[0][0])[e] = st.q[i];
+        (&k[0][0])[e] = st.k[i];
+      }
     }
-    (&x[0][0])[threadIdx.x] = kBwd ? st.d : st.v;
-    if (threadIdx.x < kBlock) {
+#pragma unroll
+    for (int i = 0; i < Stage<T, NJ, TB, RS, kBwd>::kIn; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      if (TB * kRows * RS % kThreads == 0 || e < TB * kRows * RS) (&x[0][0])[e] = st.x[i];
+    }
+    if (threadIdx.x < TB) {
       g[threadIdx.x] = st.g;
       b[threadIdx.x] = st.b;
     }
   }
 };
 
-// CTA (16 rows of the state, head, sequence), tokens in order.
-template <class T, int NJ, bool kPool>
-__global__ void __launch_bounds__(kThreads) rec_fwd_kernel(Shape s, Args a, float *__restrict__ states,
+// CTA (16 RS rows of the state, head, sequence), tokens in order.  With RS 2 a
+// group of lanes has two rows, 16 apart: twice the loads in flight where there
+// are states enough to fill the GPU.
+template <class T, int NJ, int TB, int RS, bool kPool>
+__global__ void __launch_bounds__(kThreads, NJ > 4 ? 1 : TB == 1 ? 8 : TB == 4 ? 6 : 4) rec_fwd_kernel(Shape s, Args a, float *__restrict__ states,
                                                            float *__restrict__ es, float *__restrict__ pool,
                                                            const int32_t *__restrict__ slots, int64_t nslots) {
-  __shared__ Tile<NJ> sm;
+  __shared__ Tile<NJ, TB, RS> sm;
+  constexpr int kTall = kRows * RS;
   const int lane8 = threadIdx.x & 7, r = threadIdx.x >> 3;
-  const int p0 = blockIdx.x * kRows, p = p0 + r, h = blockIdx.y;
-  const bool live = p < s.P;
+  const int p0 = blockIdx.x * kTall, h = blockIdx.y;
   T *o = static_cast<T *>(a.o);
   for (int64_t seq = blockIdx.z; seq < s.nseq; seq += gridDim.z) {
     int64_t t0, te;
@@ -141,32 +153,41 @@ __global__ void __launch_bounds__(kThreads) rec_fwd_kernel(Shape s, Args a, floa
     if (kPool) {
       if (slots != nullptr) at = slots[seq];
       if (at < 0 || at >= nslots) {   // an idle row: nothing is read or kept for it
-        for (int64_t x = threadIdx.x; x < s.T * kRows; x += kThreads) {
-          const int pp = p0 + int(x % kRows);
-          if (pp < s.P) o[((t0 + x / kRows) * s.H + h) * s.P + pp] = from_f32<T>(0.f);
+        for (int64_t x = threadIdx.x; x < s.T * kTall; x += kThreads) {
+          const int pp = p0 + int(x % kTall);
+          if (pp < s.P) o[((t0 + x / kTall) * s.H + h) * s.P + pp] = from_f32<T>(0.f);
         }
         continue;
       }
     }
     const float *from = kPool ? pool : a.init;
     float *to = kPool ? pool : a.fin;
-    const int64_t row = ((at * s.H + h) * s.P + p) * s.N;
-    float S[4 * NJ];
-    load_row<NJ>(S, live && from != nullptr ? from + row : nullptr, s.N, lane8);
-    const int64_t slot0 = kPool ? 0 : first_slot(s, a.cu, seq, t0);
-    Stage<T, NJ, false> st;
+    // the tokens' loads and the states' are in flight together
+    Stage<T, NJ, TB, RS, false> st;
     if (t0 < te) st.load(s, a, t0, te, h, p0);
-    for (int64_t b0 = t0; b0 < te; b0 += kBlock) {
-      if (!kPool && states != nullptr && live && (b0 - t0) % kChunk == 0) {
+    float S[RS][4 * NJ];
+#pragma unroll
+    for (int i = 0; i < RS; ++i) {
+      const int p = p0 + r + kRows * i;
+      load_row<NJ>(S[i], p < s.P && from != nullptr ? from + ((at * s.H + h) * s.P + p) * s.N : nullptr, s.N, lane8);
+    }
+    const int64_t slot0 = kPool ? 0 : first_slot(s, a.cu, seq, t0);
+    for (int64_t b0 = t0; b0 < te; b0 += TB) {
+      if (!kPool && states != nullptr && (b0 - t0) % kChunk == 0) {
         const int64_t slot = slot0 + (b0 - t0) / kChunk;
-        if (slot < s.slots) store_row<NJ>(S, states + ((slot * s.H + h) * s.P + p) * s.N, s.N, lane8);
+#pragma unroll
+        for (int i = 0; i < RS; ++i) {
+          const int p = p0 + r + kRows * i;
+          if (p < s.P && slot < s.slots) store_row<NJ>(S[i], states + ((slot * s.H + h) * s.P + p) * s.N, s.N, lane8);
+        }
       }
       sm.put(st);
       __syncthreads();
-      if (b0 + kBlock < te) st.load(s, a, b0 + kBlock, te, h, p0);
-      const int n = int(min(int64_t(kBlock), te - b0));
+      if (b0 + TB < te) st.load(s, a, b0 + TB, te, h, p0);
+      const int n = int(min(int64_t(TB), te - b0));
+#pragma unroll(TB == 1 ? 1 : 2)
       for (int t = 0; t < n; ++t) {
-        float kk[4 * NJ], part = 0.f, out = 0.f;
+        float kk[4 * NJ], part[RS][4] = {}, out[RS][4] = {}, u[RS];
         const float dec = sm.g[t];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -176,38 +197,52 @@ __global__ void __launch_bounds__(kThreads) rec_fwd_kernel(Shape s, Args a, floa
           kk[4 * j + 2] = kv.z;
           kk[4 * j + 3] = kv.w;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            S[4 * j + i] *= dec;
-            part = fmaf(S[4 * j + i], kk[4 * j + i], part);
-          }
+          for (int i = 0; i < RS; ++i)
+#pragma unroll
+            for (int c = 4 * j; c < 4 * j + 4; ++c) {
+              S[i][c] *= dec;
+              part[i][c & 3] = fmaf(S[i][c], kk[c], part[i][c & 3]);
+            }
         }
-        const float e = sm.x[t][r] - row_sum(part);
-        const float u = sm.b[t] * e;
+#pragma unroll
+        for (int i = 0; i < RS; ++i) {
+          const float e = sm.x[t][r + kRows * i] - row_sum((part[i][0] + part[i][1]) + (part[i][2] + part[i][3]));
+          u[i] = sm.b[t] * e;
+          if (lane8 == 0) sm.z[t][r + kRows * i] = e;
+        }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[t][(8 * j + lane8) * 4]);
           const float qq[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            S[4 * j + i] = fmaf(u, kk[4 * j + i], S[4 * j + i]);
-            out = fmaf(S[4 * j + i], qq[i], out);
-          }
+          for (int i = 0; i < RS; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              S[i][4 * j + c] = fmaf(u[i], kk[4 * j + c], S[i][4 * j + c]);
+              out[i][c] = fmaf(S[i][4 * j + c], qq[c], out[i][c]);
+            }
         }
-        out = row_sum(out);
-        if (lane8 == 0) {
-          sm.y[t][r] = a.scale * out;
-          sm.z[t][r] = e;
-        }
+#pragma unroll
+        for (int i = 0; i < RS; ++i)   // the lanes' parts are added up after the block: nothing waits for o
+          sm.y[t][r + kRows * i][lane8] = (out[i][0] + out[i][1]) + (out[i][2] + out[i][3]);
       }
       __syncthreads();
-      const int tt = threadIdx.x / kRows, rr = threadIdx.x % kRows;
-      if (tt < n && p0 + rr < s.P) {
-        const int64_t x = ((b0 + tt) * s.H + h) * s.P + p0 + rr;
-        o[x] = from_f32<T>(sm.y[tt][rr]);
-        if (es != nullptr) es[x] = sm.z[tt][rr];
+      for (int x = threadIdx.x; x < n * kTall; x += kThreads) {
+        const int tt = x / kTall, rr = x % kTall;
+        if (p0 + rr < s.P) {
+          const int64_t y = ((b0 + tt) * s.H + h) * s.P + p0 + rr;
+          const float4 u = *reinterpret_cast<const float4 *>(&sm.y[tt][rr][0]);
+          const float4 w = *reinterpret_cast<const float4 *>(&sm.y[tt][rr][4]);
+          o[y] = from_f32<T>(a.scale * (((u.x + u.y) + (u.z + u.w)) + ((w.x + w.y) + (w.z + w.w))));
+          if (es != nullptr) es[y] = sm.z[tt][rr];
+        }
       }
     }
-    if (live && to != nullptr) store_row<NJ>(S, to + row, s.N, lane8);
+#pragma unroll
+    for (int i = 0; i < RS; ++i) {
+      const int p = p0 + r + kRows * i;
+      if (p < s.P && to != nullptr) store_row<NJ>(S[i], to + ((at * s.H + h) * s.P + p) * s.N, s.N, lane8);
+    }
     __syncthreads();
   }
 }
@@ -218,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) rec_fwd_kernel(Shape s, Args a, floa
 template <class T, int NJ>
 __global__ void __launch_bounds__(kThreads) rec_bwd_kernel(Shape s, Args a, float *__restrict__ dstates,
                                                            float *__restrict__ F) {
-  __shared__ Tile<NJ> sm;
+  __shared__ Tile<NJ, kBlock, 1> sm;
   const int lane8 = threadIdx.x & 7, r = threadIdx.x >> 3;
   const int p0 = blockIdx.x * kRows, p = p0 + r, h = blockIdx.y;
   const bool live = p < s.P;
@@ -231,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) rec_bwd_kernel(Shape s, Args a, floa
     load_row<NJ>(S, live && a.dfinal != nullptr ? a.dfinal + row : nullptr, s.N, lane8);
     const int64_t slot0 = first_slot(s, a.cu, seq, t0);
     const int64_t nb = (te - t0 + kBlock - 1) / kBlock;
-    Stage<T, NJ, true> st;
+    Stage<T, NJ, kBlock, 1, true> st;
     if (nb > 0) st.load(s, a, t0 + (nb - 1) * kBlock, te, h, p0);
     for (int64_t blk = nb - 1; blk >= 0; --blk) {
       const int64_t b0 = t0 + blk * kBlock;
@@ -243,8 +278,9 @@ __global__ void __launch_bounds__(kThreads) rec_bwd_kernel(Shape s, Args a, floa
       __syncthreads();
       if (blk > 0) st.load(s, a, b0 - kBlock, te, h, p0);
       const int n = int(min(int64_t(kBlock), te - b0));
+#pragma unroll 2
       for (int t = n - 1; t >= 0; --t) {
-        float kk[4 * NJ], part = 0.f;
+        float kk[4 * NJ], part[4] = {};
         const float dec = sm.g[t], d = a.scale * sm.x[t][r];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -258,20 +294,20 @@ __global__ void __launch_bounds__(kThreads) rec_bwd_kernel(Shape s, Args a, floa
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             S[4 * j + i] = fmaf(d, qq[i], S[4 * j + i]);
-            part = fmaf(S[4 * j + i], kk[4 * j + i], part);
+            part[i] = fmaf(S[4 * j + i], kk[4 * j + i], part[i]);
           }
         }
-        const float f = row_sum(part);
+        const float f = row_sum((part[0] + part[1]) + (part[2] + part[3]));
         const float de = sm.b[t] * f;
 #pragma unroll
         for (int i = 0; i < 4 * NJ; ++i) S[i] = dec * fmaf(-de, kk[i], S[i]);
-        if (lane8 == 0) sm.y[t][r] = f;
+        if (lane8 == 0) sm.y[t][r][0] = f;
       }
       __syncthreads();
       const int tt = threadIdx.x / kRows, rr = threadIdx.x % kRows;
       if (tt < n && p0 + rr < s.P) {
         const int64_t x = ((b0 + tt) * s.H + h) * s.P + p0 + rr;
-        const float f = sm.y[tt][rr];
+        const float f = sm.y[tt][rr][0];
         F[x] = f;
         dv[x] = from_f32<T>(sm.b[tt] * f);
       }
@@ -530,24 +566,40 @@ Work carve_work(const Shape &s, void *p) {
   return o;
 }
 
-dim3 rec_grid(const Shape &s) {
-  return dim3(unsigned((s.P + kRows - 1) / kRows), unsigned(s.H), unsigned(s.nseq < 65535 ? s.nseq : 65535));
+dim3 rec_grid(const Shape &s, int rows) {
+  return dim3(unsigned((s.P + rows - 1) / rows), unsigned(s.H), unsigned(s.nseq < 65535 ? s.nseq : 65535));
 }
 
-template <class T, bool kPool>
+template <class T, int TB, int RS, bool kPool>
 cudaError_t launch_fwd(const Shape &s, const Args &a, float *states, float *es, float *pool, const int32_t *slots,
                        int64_t nslots, cudaStream_t st) {
-  const dim3 grid = rec_grid(s);
-  if (s.N <= 32) rec_fwd_kernel<T, 1, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
-  else if (s.N <= 64) rec_fwd_kernel<T, 2, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
-  else if (s.N <= 128) rec_fwd_kernel<T, 4, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
-  else rec_fwd_kernel<T, 8, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  const dim3 grid = rec_grid(s, kRows * RS);
+  if (s.N <= 32) rec_fwd_kernel<T, 1, TB, RS, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  else if (s.N <= 64) rec_fwd_kernel<T, 2, TB, RS, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  else if (s.N <= 128) rec_fwd_kernel<T, 4, TB, RS, kPool><<<grid, kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
+  else rec_fwd_kernel<T, 8, TB, 1, kPool><<<rec_grid(s, kRows), kThreads, 0, st>>>(s, a, states, es, pool, slots, nslots);
   return cudaGetLastError();
 }
 
 template <class T>
+cudaError_t launch_step(const Shape &s, const Args &a, float *pool, const int32_t *slots, int64_t nslots,
+                        cudaStream_t st) {
+  // a block of tokens no longer than the step, and two rows a group of lanes where that still gives every SM eight CTAs
+  const bool two = s.nseq * s.H * ((s.P + 2 * kRows - 1) / (2 * kRows)) >= 8 * 152;
+  if (s.T == 1) {
+    return two ? launch_fwd<T, 1, 2, true>(s, a, nullptr, nullptr, pool, slots, nslots, st)
+               : launch_fwd<T, 1, 1, true>(s, a, nullptr, nullptr, pool, slots, nslots, st);
+  }
+  if (s.T <= 4) {
+    return two ? launch_fwd<T, 4, 2, true>(s, a, nullptr, nullptr, pool, slots, nslots, st)
+               : launch_fwd<T, 4, 1, true>(s, a, nullptr, nullptr, pool, slots, nslots, st);
+  }
+  return launch_fwd<T, kBlock, 1, true>(s, a, nullptr, nullptr, pool, slots, nslots, st);
+}
+
+template <class T>
 cudaError_t launch_bwd(const Shape &s, const Args &a, const Saved &sv, const Work &w, cudaStream_t st) {
-  const dim3 grid = rec_grid(s);
+  const dim3 grid = rec_grid(s, kRows);
   if (s.N <= 32) rec_bwd_kernel<T, 1><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
   else if (s.N <= 64) rec_bwd_kernel<T, 2><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
   else if (s.N <= 128) rec_bwd_kernel<T, 4><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
@@ -569,14 +621,14 @@ size_t general_bwd_workspace(const Shape &s) { return carve_work(s, nullptr).byt
 cudaError_t general_fwd(const Shape &s, bool bf16, const Args &a, void *saved, cudaStream_t st) {
   Saved sv{};
   if (saved != nullptr) sv = carve_saved(s, saved);
-  return bf16 ? launch_fwd<__nv_bfloat16, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st)
-              : launch_fwd<float, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st);
+  return bf16 ? launch_fwd<__nv_bfloat16, kBlock, 1, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st)
+              : launch_fwd<float, kBlock, 1, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st);
 }
 
 cudaError_t general_step(const Shape &s, bool bf16, const Args &a, float *pool, const int32_t *slots, int64_t nslots,
                          cudaStream_t st) {
-  return bf16 ? launch_fwd<__nv_bfloat16, true>(s, a, nullptr, nullptr, pool, slots, nslots, st)
-              : launch_fwd<float, true>(s, a, nullptr, nullptr, pool, slots, nslots, st);
+  return bf16 ? launch_step<__nv_bfloat16>(s, a, pool, slots, nslots, st)
+              : launch_step<float>(s, a, pool, slots, nslots, st);
 }
 
 cudaError_t general_bwd(const Shape &s, bool bf16, const Args &a, const void *saved, void *ws, cudaStream_t st) {

@@ -17,7 +17,11 @@
 //     D / 16 lanes a row; D 32, 64, 128 or 256, R a multiple of 16, rows on
 //     16-byte boundaries;
 //   - narrow: one pair at a time, a warp a row; any D up to 512.
-// A thread's cos and sin serve kHeads heads of the same token.
+// A CTA takes a tile of consecutive tokens and a range of the heads of q or of
+// k, so that a token's cos and sin are read once for all of them; the heads
+// are cut into as many ranges as it takes to fill the GPU when tokens are few.
+// Loads of kHeads heads are in flight at once in each of 3 (backward: 2) CTAs
+// an SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -31,8 +35,9 @@ namespace {
 using ssd::ld;
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;       // heads of a token that one group of lanes takes together
-constexpr int kParts = 608;     // fixed CTAs (and partial sums) of the weight gradients of q, and of k
+constexpr int kHeads = 2;       // heads of a token that one group of lanes takes together
+constexpr int kParts = 304;     // at most so many CTAs (and partial sums) of the weight gradients of q, and of k
+constexpr int kFill = 608;      // CTAs that fill the GPU (four on each of 152 SMs)
 
 struct Side {                   // q or k
   const void *x, *dz;
@@ -49,26 +54,32 @@ struct Params {
   int64_t tokens, npos;
   int D, R, interleaved, rms;
   float eps;
-  unsigned blocks0;             // CTAs of side 0
+  int ranges0;                  // ranges that the heads of side 0 are cut into (gridDim.y counts both sides')
 };
 
+// A run of V elements as loaded, opened to fp32 when it is worked on.
 template <int V, class T>
-__device__ __forceinline__ void load_run(const T *p, float (&o)[V]) {
-  if constexpr (V == 1) {
-    o[0] = ld(p);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Run {
+  uint32_t w[V == 1 ? 1 : V * sizeof(T) / 4];
+  __device__ __forceinline__ void load(const T *p, bool on) {
+    if constexpr (V == 1) {
+      w[0] = on ? __float_as_uint(ld(p)) : 0u;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __uint_as_float(w[i] << 16);
-      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int i = 0; i < int(V * sizeof(T) / 16); ++i) {
+        const uint4 u = on ? reinterpret_cast<const uint4 *>(p)[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+      }
     }
-  } else {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
   }
-}
+  __device__ __forceinline__ void open(float (&o)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (V == 1 || sizeof(T) == 4) o[i] = __uint_as_float(w[i]);
+      else o[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+  }
+};
 template <int V, class T>
 __device__ __forceinline__ void store_run(T *p, const float (&v)[V]) {
   if constexpr (V == 1) {
@@ -148,16 +159,16 @@ __device__ __forceinline__ void turn(bool inter, float (&xa)[V], float (&xb)[V],
 
 // L lanes a row, each with PT units of two runs of V elements.
 template <class T, int V, int L, int PT, bool kBwd, bool kHasW>
-__global__ void __launch_bounds__(kThreads) qk_kernel(Params q) {
-  constexpr int kGroups = kThreads / L;        // rows of a CTA at a time
+__global__ void __launch_bounds__(kThreads, V == 1 ? 1 : (kBwd ? 2 : 3)) qk_kernel(Params q) {
+  constexpr int kGroups = kThreads / L;        // tokens of a CTA at a time
   constexpr int HB = V == 1 ? 1 : kHeads;
-  const int which = blockIdx.x >= q.blocks0;
+  const int which = int(blockIdx.y) >= q.ranges0;
   const Side sd = q.side[which];
-  const unsigned block = which ? blockIdx.x - q.blocks0 : blockIdx.x;
-  const unsigned blocks = which ? gridDim.x - q.blocks0 : q.blocks0;
+  const int range = which ? blockIdx.y - q.ranges0 : blockIdx.y, ranges = which ? gridDim.y - q.ranges0 : q.ranges0;
+  const int block = blockIdx.x * ranges + range;   // of this side
   const int lane = threadIdx.x % L, grp = threadIdx.x / L;
   const int sets = (sd.heads + HB - 1) / HB;
-  const int64_t units = q.tokens * sets;
+  const int set0 = int(int64_t(sets) * range / ranges), set1 = int(int64_t(sets) * (range + 1) / ranges);
   const float over = q.rms ? 1.f / float(q.D) : 1.f;
   const T *x = static_cast<const T *>(sd.x);
   const T *dz = static_cast<const T *>(sd.dz);
@@ -177,32 +188,10 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(Params q) {
       }
     }
   }
-  // every lane of a warp takes part in the shuffles, so the loop is uniform over the CTA
-  for (int64_t u0 = int64_t(block) * kGroups; u0 < units; u0 += int64_t(blocks) * kGroups) {
-    const int64_t unit = u0 + grp;
-    const bool live = unit < units;
-    const int64_t tok = live ? unit / sets : 0;
-    const int h0 = live ? int(unit % sets) * HB : 0;
-    float xa[HB][PT][V], xb[HB][PT][V], da[kBwd ? HB : 1][PT][V], db[kBwd ? HB : 1][PT][V];
-#pragma unroll
-    for (int h = 0; h < HB; ++h)
-#pragma unroll
-      for (int u = 0; u < PT; ++u) {
-        const Place p = place<V>(q, lane + u * L);
-        const bool on = live && h0 + h < sd.heads;
-        const T *row = x + tok * sd.stride + int64_t(h0 + h) * q.D;
-        const T *drow = dz + (tok * sd.heads + h0 + h) * q.D;
-        if (on && p.na) load_run<V>(row + p.a, xa[h][u]);
-        if (on && p.nb) load_run<V>(row + p.b, xb[h][u]);
-        if (kBwd && on && p.na) load_run<V>(drow + p.a, da[h][u]);
-        if (kBwd && on && p.nb) load_run<V>(drow + p.b, db[h][u]);
-        if (!(on && p.na))
-#pragma unroll
-          for (int i = 0; i < V; ++i) xa[h][u][i] = 0.f, da[kBwd ? h : 0][u][i] = 0.f;
-        if (!(on && p.nb))
-#pragma unroll
-          for (int i = 0; i < V; ++i) xb[h][u][i] = 0.f, db[kBwd ? h : 0][u][i] = 0.f;
-      }
+  // every lane of a warp takes part in the shuffles, so the loops are uniform over the CTA
+  for (int64_t t0 = int64_t(blockIdx.x) * kGroups; t0 < q.tokens; t0 += int64_t(gridDim.x) * kGroups) {
+    const bool live = t0 + grp < q.tokens;
+    const int64_t tok = live ? t0 + grp : 0;
     float c[PT][V], s[PT][V];
     bool bad = false;
     if (q.R > 0) {
@@ -212,68 +201,92 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(Params q) {
       for (int u = 0; u < PT; ++u) {
         const Place p = place<V>(q, lane + u * L);
         const bool on = p.rot && !bad;
-#pragma unroll
-        for (int i = 0; i < V; ++i) c[u][i] = 1.f, s[u][i] = 0.f;
-        if (on) {
-          load_run<V>(q.cos + at * (q.R / 2) + p.angle, c[u]);
-          load_run<V>(q.sin + at * (q.R / 2) + p.angle, s[u]);
-        }
+        Run<V, float> rc, rs;
+        rc.load(q.cos + at * (q.R / 2) + p.angle, on);
+        rs.load(q.sin + at * (q.R / 2) + p.angle, on);
+        rc.open(c[u]);
+        rs.open(s[u]);
       }
     }
+#pragma unroll 1
+    for (int h0 = set0 * HB; h0 < set1 * HB; h0 += HB) {
+      Run<V, T> xa[HB][PT], xb[HB][PT], da[kBwd ? HB : 1][PT], db[kBwd ? HB : 1][PT];
 #pragma unroll
-    for (int h = 0; h < HB; ++h) {
-      float ss = 0.f;
-#pragma unroll
-      for (int u = 0; u < PT; ++u)
-#pragma unroll
-        for (int i = 0; i < V; ++i) ss = fmaf(xa[h][u][i], xa[h][u][i], fmaf(xb[h][u][i], xb[h][u][i], ss));
-      ss = lanes_sum<L>(ss);
-      // rows outside the problem stay zero even where eps is
-      float r = live && h0 + h < sd.heads ? rsqrtf(fmaf(ss, over, q.eps)) : 0.f;
-      if (bad) r = __int_as_float(0x7fc00000);
-      float dot = 0.f;
-#pragma unroll
-      for (int u = 0; u < PT; ++u) {
-        const Place p = place<V>(q, lane + u * L);
-#pragma unroll
-        for (int i = 0; i < V; ++i) xa[h][u][i] *= r, xb[h][u][i] *= r;   // the normed row
-        if (!kBwd) {
-          if (kHasW)
-#pragma unroll
-            for (int i = 0; i < V; ++i) xa[h][u][i] *= wa[u][i], xb[h][u][i] *= wb[u][i];
-          if (p.rot) turn<V>(inter, xa[h][u], xb[h][u], c[u], s[u], 1.f);
-        } else {
-          if (p.rot) turn<V>(inter, da[h][u], db[h][u], c[u], s[u], -1.f);
-          if (kHasW) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              ga[u][i] = fmaf(da[h][u][i], xa[h][u][i], ga[u][i]);
-              gb[u][i] = fmaf(db[h][u][i], xb[h][u][i], gb[u][i]);
-              da[h][u][i] *= wa[u][i];
-              db[h][u][i] *= wb[u][i];
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) dot = fmaf(da[h][u][i], xa[h][u][i], fmaf(db[h][u][i], xb[h][u][i], dot));
-        }
-      }
-      if (kBwd) {
-        dot = lanes_sum<L>(dot) * over;
-#pragma unroll
-        for (int u = 0; u < PT; ++u)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            xa[h][u][i] = r * fmaf(-xa[h][u][i], dot, da[h][u][i]);
-            xb[h][u][i] = r * fmaf(-xb[h][u][i], dot, db[h][u][i]);
-          }
-      }
-      if (live && h0 + h < sd.heads) {
-        T *row = out + (tok * sd.heads + h0 + h) * q.D;
+      for (int h = 0; h < HB; ++h)
 #pragma unroll
         for (int u = 0; u < PT; ++u) {
           const Place p = place<V>(q, lane + u * L);
-          if (p.na) store_run<V>(row + p.a, xa[h][u]);
-          if (p.nb) store_run<V>(row + p.b, xb[h][u]);
+          const bool on = live && h0 + h < sd.heads;
+          const T *row = x + tok * sd.stride + int64_t(h0 + h) * q.D;
+          xa[h][u].load(row + p.a, on && p.na);
+          xb[h][u].load(row + p.b, on && p.nb);
+          if (kBwd) {
+            const T *drow = dz + (tok * sd.heads + h0 + h) * q.D;
+            da[h][u].load(drow + p.a, on && p.na);
+            db[h][u].load(drow + p.b, on && p.nb);
+          }
+        }
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+        float va[PT][V], vb[PT][V], ss = 0.f;
+#pragma unroll
+        for (int u = 0; u < PT; ++u) {
+          xa[h][u].open(va[u]);
+          xb[h][u].open(vb[u]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) ss = fmaf(va[u][i], va[u][i], fmaf(vb[u][i], vb[u][i], ss));
+        }
+        ss = lanes_sum<L>(ss);
+        // rows outside the problem stay zero even where eps is
+        float r = live && h0 + h < sd.heads ? rsqrtf(fmaf(ss, over, q.eps)) : 0.f;
+        if (bad) r = __int_as_float(0x7fc00000);
+        if (!kBwd) {
+#pragma unroll
+          for (int u = 0; u < PT; ++u) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              va[u][i] *= kHasW ? r * wa[u][i] : r;
+              vb[u][i] *= kHasW ? r * wb[u][i] : r;
+            }
+            if (place<V>(q, lane + u * L).rot) turn<V>(inter, va[u], vb[u], c[u], s[u], 1.f);
+          }
+        } else {
+          float ua[PT][V], ub[PT][V], dot = 0.f;
+#pragma unroll
+          for (int u = 0; u < PT; ++u) {
+            da[h][u].open(ua[u]);
+            db[h][u].open(ub[u]);
+            if (place<V>(q, lane + u * L).rot) turn<V>(inter, ua[u], ub[u], c[u], s[u], -1.f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              va[u][i] *= r;   // the normed row
+              vb[u][i] *= r;
+              if (kHasW) {
+                ga[u][i] = fmaf(ua[u][i], va[u][i], ga[u][i]);
+                gb[u][i] = fmaf(ub[u][i], vb[u][i], gb[u][i]);
+                ua[u][i] *= wa[u][i];
+                ub[u][i] *= wb[u][i];
+              }
+              dot = fmaf(ua[u][i], va[u][i], fmaf(ub[u][i], vb[u][i], dot));
+            }
+          }
+          dot = lanes_sum<L>(dot) * over;
+#pragma unroll
+          for (int u = 0; u < PT; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              va[u][i] = r * fmaf(-va[u][i], dot, ua[u][i]);
+              vb[u][i] = r * fmaf(-vb[u][i], dot, ub[u][i]);
+            }
+        }
+        if (live && h0 + h < sd.heads) {
+          T *row = out + (tok * sd.heads + h0 + h) * q.D;
+#pragma unroll
+          for (int u = 0; u < PT; ++u) {
+            const Place p = place<V>(q, lane + u * L);
+            if (p.na) store_run<V>(row + p.a, va[u]);
+            if (p.nb) store_run<V>(row + p.b, vb[u]);
+          }
         }
       }
     }
@@ -317,13 +330,13 @@ __global__ void weight_fold_kernel(const float *__restrict__ part0, const float 
 }
 
 template <class T, int V, int L, int PT, bool kBwd>
-void launch(const Params &q, unsigned blocks, bool has_w, cudaStream_t st) {
+void launch(const Params &q, dim3 blocks, bool has_w, cudaStream_t st) {
   if (has_w) qk_kernel<T, V, L, PT, kBwd, true><<<blocks, kThreads, 0, st>>>(q);
   else qk_kernel<T, V, L, PT, kBwd, false><<<blocks, kThreads, 0, st>>>(q);
 }
 
 template <class T, bool kBwd>
-void launch_form(const Params &q, bool wide, unsigned blocks, bool has_w, cudaStream_t st) {
+void launch_form(const Params &q, bool wide, dim3 blocks, bool has_w, cudaStream_t st) {
   if (wide) {
     switch (q.D) {
       case 32: return launch<T, 8, 2, 1, kBwd>(q, blocks, has_w, st);
@@ -343,7 +356,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool dims_ok(const ssd_qk_dims *d) {
   if (d == nullptr || d->tokens < 0 || d->qheads < 1 || d->kheads < 1 || d->headdim < 1 || d->headdim > 512)
     return false;
-  if (d->tokens > (int64_t(1) << 40) || d->qheads > 65536 || d->kheads > 65536) return false;
+  if (d->tokens > (int64_t(1) << 40) || d->qheads > 32768 || d->kheads > 32768) return false;
   if (d->rotary < 0 || d->rotary > d->headdim || d->rotary % 2 != 0) return false;
   if (d->rotary > 0 && (d->positions < 1 || d->positions > (int64_t(1) << 31))) return false;
   if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return false;
@@ -405,21 +418,25 @@ ssd_status run(const ssd_qk_dims *d, bool bwd, const void *q, const void *k, con
   const bool wide = (D == 32 || D == 64 || D == 128 || D == 256) && d->rotary % 16 == 0 && aligned16(q) &&
                     aligned16(k) && aligned16(oq) && aligned16(ok) && aligned16(dq_in) && aligned16(dk_in) &&
                     aligned16(cos) && aligned16(sin) && size_t(qs) * el % 16 == 0 && size_t(ks) * el % 16 == 0;
-  // CTAs in proportion to the heads of each side; with weight gradients at most kParts a side, whatever the device
   const int groups = wide ? kThreads / (D / 16) : kThreads / 32;
-  auto ctas = [&](int heads, int64_t cap) {
+  const int64_t tiles = (d->tokens + groups - 1) / groups;
+  auto ranges = [&](int heads) {   // enough that tiles * ranges fill the GPU, half for each side
     const int64_t sets = wide ? (heads + kHeads - 1) / kHeads : heads;
-    const int64_t want = (d->tokens * sets + groups - 1) / groups;
-    return unsigned(want < cap ? want : cap);
+    const int64_t want = (kFill / 2 + tiles - 1) / tiles;
+    return int(want < sets ? want : sets);
   };
-  const int64_t cap = bwd && has_w ? kParts : int64_t(1) << 16;
-  p.blocks0 = ctas(d->qheads, cap);
-  const unsigned blocks1 = ctas(d->kheads, cap);
+  p.ranges0 = ranges(d->qheads);
+  const int ranges1 = ranges(d->kheads);
+  int64_t columns = tiles < (int64_t(1) << 30) ? tiles : int64_t(1) << 30;
+  if (bwd && has_w) {   // as many partial rows as there is room for, whatever the device
+    const int most = p.ranges0 > ranges1 ? p.ranges0 : ranges1;
+    if (columns > kParts / most) columns = kParts / most;
+  }
   if (bwd && has_w) {
     p.side[0].part = static_cast<float *>(ws);
     p.side[1].part = static_cast<float *>(ws) + int64_t(kParts) * D;
   }
-  const unsigned blocks = p.blocks0 + blocks1;
+  const dim3 blocks(unsigned(columns), unsigned(p.ranges0 + ranges1));
   if (d->dtype == SSD_BF16) {
     if (bwd) launch_form<__nv_bfloat16, true>(p, wide, blocks, has_w, st);
     else launch_form<__nv_bfloat16, false>(p, wide, blocks, has_w, st);
@@ -428,8 +445,9 @@ ssd_status run(const ssd_qk_dims *d, bool bwd, const void *q, const void *k, con
     else launch_form<float, false>(p, wide, blocks, has_w, st);
   }
   if (bwd && has_w)
-    weight_fold_kernel<<<dim3(unsigned((D + 7) / 8), 2), 256, 0, st>>>(p.side[0].part, p.side[1].part, int(p.blocks0),
-                                                                       int(blocks1), D, dwq, dwk);
+    weight_fold_kernel<<<dim3(unsigned((D + 7) / 8), 2), 256, 0, st>>>(p.side[0].part, p.side[1].part,
+                                                                       int(columns) * p.ranges0, int(columns) * ranges1, D, dwq,
+                                                                       dwk);
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

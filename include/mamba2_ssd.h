@@ -412,7 +412,7 @@ typedef struct {
   int64_t tokens;              /* rows of q and k; 0 launches nothing */
   int64_t q_stride, k_stride;  /* elements between consecutive tokens; 0: packed (heads * headdim) */
   int64_t positions;           /* rows of the cosine and sine tables (rotary > 0) */
-  int32_t qheads, kheads;      /* 1..65536 */
+  int32_t qheads, kheads;      /* 1..32768 */
   int32_t headdim;             /* 1..512 */
   int32_t rotary;              /* even, 0..headdim */
   int32_t interleaved;         /* 0 or 1 */
