@@ -18,7 +18,7 @@ __all__ = ["lib", "fwd", "bwd", "Saved", "SsdError", "make_dims", "num_configs",
            "bwd_workspace_size", "fwd_workspace_size", "bwd_num_launches", "bwd_launch_names", "LIB_PATH",
            "dt_fwd", "dt_bwd", "gate_fwd", "gate_bwd", "conv1d_fwd", "conv1d_bwd", "SSDFunction", "ssd",
            "qk_fwd", "qk_bwd", "QkFunction", "qk_norm", "delta_fwd", "delta_bwd", "delta_prefill", "delta_step",
-           "delta_check", "delta_workspace_size", "DeltaSaved", "DeltaFunction", "delta", "make_delta_dims", "make_qk_dims", "delta_path_name"]
+           "DeltaSaved", "DeltaFunction", "delta", "make_delta_dims", "make_qk_dims", "delta_path_name"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmamba2_ssd.so")
 
@@ -443,6 +443,5 @@ def ssd(x, dt, A, B, C, D, chunk_size, seq_idx=None, init_states=None, any_start
 # (at the end: the module uses the helpers above)
 
 from . import _delta  # noqa: E402
-from ._delta import (DeltaFunction, DeltaSaved, QkFunction, delta, delta_bwd, delta_check, delta_fwd,  # noqa: E402
-                     delta_path_name, delta_prefill, delta_step, delta_workspace_size, make_delta_dims, make_qk_dims,
-                     qk_bwd, qk_fwd, qk_norm)
+from ._delta import (DeltaFunction, DeltaSaved, QkFunction, delta, delta_bwd, delta_fwd, delta_path_name,  # noqa: E402
+                     delta_prefill, delta_step, make_delta_dims, make_qk_dims, qk_bwd, qk_fwd, qk_norm)

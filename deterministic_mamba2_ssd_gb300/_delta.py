@@ -47,7 +47,6 @@ def declare(L):
             ("delta_path_name", ctypes.c_char_p, [pd]),
             ("delta_fwd", ctypes.c_int, [pd] + [vp] * 7 + [f32] + [vp] * 3 + [sz, vp, sz, vp]),
             ("delta_bwd", ctypes.c_int, [pd] + [vp] * 5 + [f32, vp, sz] + [vp] * 9 + [sz, vp]),
-            ("delta_check", ctypes.c_int, [pd, vp, vp]),
             ("delta_step", ctypes.c_int, [pd] + [vp] * 5 + [f32, vp, i64, vp, vp, vp])):
         f = getattr(L, "mamba2_ssd_" + name)
         f.argtypes, f.restype = args, res
@@ -311,10 +310,10 @@ def _delta_run(q, k, v, g, beta, scale, cu_seqlens, init_states, want_final, wan
         final = torch.empty((dims.nseq, dims.nheads, dims.headdim, dims.dstate), dtype=torch.float32,
                             device=dev) if want_final else None
         saved = torch.empty(saved_bytes, dtype=torch.uint8, device=dev) if want_saved else None
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws = None if want_saved else torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         rc = lib().mamba2_ssd_delta_fwd(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                         _at(cu_seqlens), _at(init_states), scale, o.data_ptr(), _at(final), _at(saved),
-                                        saved_bytes if want_saved else 0, ws.data_ptr(), ws_bytes, st)
+                                        saved_bytes if want_saved else 0, _at(ws), 0 if want_saved else ws_bytes, st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_delta_fwd")
     keep = dict(q=q, k=k, g=g, beta=beta, cu_seqlens=cu_seqlens, init=init_states, saved=saved, final=final)
@@ -336,10 +335,9 @@ def delta_prefill(q, k, v, g, beta, scale=None, init_states=None, cu_seqlens=Non
     return _delta_run(q, k, v, g, beta, scale, cu_seqlens, init_states, True, False, stream)[:2]
 
 
-def delta_bwd(saved: DeltaSaved, dout, dfinal=None, want_dinit=None, stream=None, workspace=None):
+def delta_bwd(saved: DeltaSaved, dout, dfinal=None, want_dinit=None, stream=None):
     """dict of dq, dk, dv, dg, dbeta (in q's dtype) and, with initial states
-    (or want_dinit), dinit (fp32) of sum(o * dout) + sum(final * dfinal).
-    ``workspace`` may supply a uint8 buffer (see delta_check)."""
+    (or want_dinit), dinit (fp32) of sum(o * dout) + sum(final * dfinal)."""
     t, d = saved.tensors, saved.dims
     q, k = t["q"], t["k"]
     dev, dt = q.device, q.dtype
@@ -358,12 +356,12 @@ def delta_bwd(saved: DeltaSaved, dout, dfinal=None, want_dinit=None, stream=None
                    dbeta=torch.empty(shape[:3], dtype=dt, device=dev))
         if want_dinit:
             out["dinit"] = torch.empty(states, dtype=torch.float32, device=dev)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
         rc = lib().mamba2_ssd_delta_bwd(at, q.data_ptr(), k.data_ptr(), t["g"].data_ptr(), t["beta"].data_ptr(),
                                         _at(t["cu_seqlens"]), saved.scale, t["saved"].data_ptr(), saved_bytes,
                                         dout.data_ptr(), _at(dfinal), out["dq"].data_ptr(), out["dk"].data_ptr(),
                                         out["dv"].data_ptr(), out["dg"].data_ptr(), out["dbeta"].data_ptr(),
-                                        _at(out.get("dinit")), ws.data_ptr(), ws.numel(), st)
+                                        _at(out.get("dinit")), ws.data_ptr(), need, st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_delta_bwd")
     return out
@@ -380,17 +378,6 @@ def _step_plan(q, k, v, g, beta, states, slots):
     elif n < dims.batch:
         raise ValueError("fewer states than rows")
     return dims, at
-
-
-def delta_workspace_size(saved: DeltaSaved) -> int:
-    """Bytes of the workspace of a backward."""
-    return saved.plan[4]
-
-
-def delta_check(saved: DeltaSaved, workspace=None, stream=None):
-    """Status code (0: fine) that the device left in the forward's record, or in the workspace given to a backward."""
-    at = _at(saved.tensors["saved"] if workspace is None else workspace)
-    return lib().mamba2_ssd_delta_check(saved.plan[1], at, _scope(saved.tensors["q"].device, stream)[1])
 
 
 def delta_step(q, k, v, g, beta, states, slots=None, scale=None, stream=None):

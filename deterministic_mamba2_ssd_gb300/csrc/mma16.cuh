@@ -96,28 +96,23 @@ __device__ __forceinline__ float pow2_above(float m) {
 // 1 / s of a power of two s = 2^e, |e| <= 126, exactly.
 __device__ __forceinline__ float pow2_inv(float s) { return __uint_as_float(0x7F000000u - __float_as_uint(s)); }
 
-// Addresses of this lane's row in the four-matrix loads below; `at(row, chunk)` is a tile's layout.
-//
-// B operands from a tile [n][k]: matrices (n0, k0), (n0, k0+8), (n0+8, k0), (n0+8, k0+8) -- b0, b1 of the column tile at
-// n0 and b0, b1 of the one at n0 + 8.
-template <class At>
-__device__ __forceinline__ uint32_t b_addr(At at, int n0, int k0, int lane) {
-  return at(n0 + (lane & 7) + ((lane >> 4) << 3), (k0 >> 3) + ((lane >> 3) & 1));
+// Address of this lane's row in a four-matrix load of B operands: matrices
+// (n0, k0), (n0, k0+8), (n0+8, k0), (n0+8, k0+8) of a tile [n][k], giving b0,
+// b1 of the n-tile at n0 and b0, b1 of the one at n0 + 8.
+__device__ __forceinline__ uint32_t b_addr(uint32_t tile, int n0, int k0, int bytes, int lane) {
+  return tile + swz(n0 + (lane & 7) + ((lane >> 4) << 3), (k0 >> 3) + ((lane >> 3) & 1), bytes);
 }
 // The same operands from a tile [k][n] (transposing load): matrices (k0, n0), (k0+8, n0), (k0, n0+8), (k0+8, n0+8).
-template <class At>
-__device__ __forceinline__ uint32_t bt_addr(At at, int n0, int k0, int lane) {
-  return at(k0 + (lane & 7) + (((lane >> 3) & 1) << 3), (n0 >> 3) + (lane >> 4));
+__device__ __forceinline__ uint32_t bt_addr(uint32_t tile, int n0, int k0, int bytes, int lane) {
+  return tile + swz(k0 + (lane & 7) + (((lane >> 3) & 1) << 3), (n0 >> 3) + (lane >> 4), bytes);
 }
 // A operand 16 x 16 at (m0, k0) of a tile [m][k].
-template <class At>
-__device__ __forceinline__ uint32_t a_addr(At at, int m0, int k0, int lane) {
-  return at(m0 + (lane & 7) + (((lane >> 3) & 1) << 3), (k0 >> 3) + (lane >> 4));
+__device__ __forceinline__ uint32_t a_addr(uint32_t tile, int m0, int k0, int bytes, int lane) {
+  return tile + swz(m0 + (lane & 7) + (((lane >> 3) & 1) << 3), (k0 >> 3) + (lane >> 4), bytes);
 }
 // A operand 16 x 16 at (m0, k0) of a tile [k][m] (transposing load).
-template <class At>
-__device__ __forceinline__ uint32_t at_addr(At at, int m0, int k0, int lane) {
-  return at(k0 + (lane & 7) + ((lane >> 4) << 3), (m0 >> 3) + ((lane >> 3) & 1));
+__device__ __forceinline__ uint32_t at_addr(uint32_t tile, int m0, int k0, int bytes, int lane) {
+  return tile + swz(k0 + (lane & 7) + ((lane >> 4) << 3), (m0 >> 3) + ((lane >> 3) & 1), bytes);
 }
 
 }  // namespace mma16

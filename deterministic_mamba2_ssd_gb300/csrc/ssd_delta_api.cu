@@ -86,13 +86,12 @@ extern "C" {
 size_t mamba2_ssd_delta_saved_size(const ssd_delta_dims *dims) {
   if (!dims_ok(dims)) return 0;
   const Shape s = shape_of(dims);
-  return 256 + (tiles_path(dims) ? ssd::delta::carve_tiles(s, nullptr, nullptr, true, 1).rec_bytes
-                                 : ssd::delta::general_saved(s));
+  return 256 + (tiles_path(dims) ? ssd::delta::carve_tiles(s, nullptr, true).bytes : ssd::delta::general_saved(s));
 }
 
 size_t mamba2_ssd_delta_fwd_workspace_size(const ssd_delta_dims *dims) {
   if (!dims_ok(dims)) return 0;
-  return 256 + (tiles_path(dims) ? ssd::delta::carve_tiles(shape_of(dims), nullptr, nullptr, false, 2).work_bytes : 0);
+  return 256 + (tiles_path(dims) ? ssd::delta::carve_tiles(shape_of(dims), nullptr, false).bytes : 0);
 }
 
 size_t mamba2_ssd_delta_bwd_workspace_size(const ssd_delta_dims *dims) {
@@ -117,16 +116,17 @@ ssd_status mamba2_ssd_delta_fwd(const ssd_delta_dims *dims, const void *q, const
     return SSD_ERR_INVALID_ARG;
   if (s.total > 0 && (!acts_ok(dims, {q, k, v, o}) || !floats_ok({g, beta}))) return SSD_ERR_INVALID_ARG;
   if (saved != nullptr && saved_bytes < mamba2_ssd_delta_saved_size(dims)) return SSD_ERR_WORKSPACE;
-  if (workspace_bytes < mamba2_ssd_delta_fwd_workspace_size(dims)) return SSD_ERR_WORKSPACE;
-  if (workspace == nullptr) return SSD_ERR_INVALID_ARG;
+  if (saved == nullptr) {
+    if (workspace_bytes < mamba2_ssd_delta_fwd_workspace_size(dims)) return SSD_ERR_WORKSPACE;
+    if (workspace == nullptr) return SSD_ERR_INVALID_ARG;
+  }
   Args a{};
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.cu = cu_seqlens, a.init = init_states, a.o = o;
   a.fin = final_states, a.scale = scale;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!tiles_path(dims)) return status_of(ssd::delta::general_fwd(s, bf16_of(dims), a, saved, st));
-  const ssd::delta::Tiles t =
-      ssd::delta::carve_tiles(s, saved, workspace, saved != nullptr, final_states != nullptr ? 2 : 1);
-  const cudaError_t e = ssd::delta::launch_prep(s, a, t, st);
+  const ssd::delta::Tiles t = ssd::delta::carve_tiles(s, saved != nullptr ? saved : workspace, saved != nullptr);
+  const cudaError_t e = ssd::delta::launch_prep(s, a, t, final_states != nullptr, st);
   return status_of(e != cudaSuccess ? e : ssd::delta::launch_chain_fwd(s, a, t, st));
 }
 
@@ -151,22 +151,10 @@ ssd_status mamba2_ssd_delta_bwd(const ssd_delta_dims *dims, const void *q, const
   a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dinit = dinit;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!tiles_path(dims)) return status_of(ssd::delta::general_bwd(s, bf16_of(dims), a, saved, workspace, st));
-  const ssd::delta::Tiles t = ssd::delta::carve_tiles(s, const_cast<void *>(saved), nullptr, true, 1);
+  const ssd::delta::Tiles t = ssd::delta::carve_tiles(s, const_cast<void *>(saved), true);
   const ssd::delta::BwdTiles w = ssd::delta::carve_bwd_tiles(s, workspace);
-  cudaError_t e = ssd::delta::launch_prep_bwd(s, a, t, w, st);
-  if (e == cudaSuccess) e = ssd::delta::launch_chain_bwd(s, a, t, w, st);
+  const cudaError_t e = ssd::delta::launch_chain_bwd(s, a, t, w, st);
   return status_of(e != cudaSuccess ? e : ssd::delta::launch_grads(s, a, t, w, st));
-}
-
-ssd_status mamba2_ssd_delta_check(const ssd_delta_dims *dims, const void *record_or_workspace, void *stream) {
-  if (!dims_ok(dims) || record_or_workspace == nullptr || !aligned(record_or_workspace, 16)) return SSD_ERR_INVALID_ARG;
-  if (!tiles_path(dims)) return SSD_OK;
-  int word = 0;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemcpyAsync(&word, record_or_workspace, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return SSD_ERR_CUDA;
-  return word == 0 ? SSD_OK : word == 1 ? SSD_ERR_TIMEOUT : SSD_ERR_UNSUPPORTED;
 }
 
 ssd_status mamba2_ssd_delta_step(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,

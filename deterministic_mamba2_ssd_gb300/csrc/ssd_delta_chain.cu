@@ -1,106 +1,174 @@
-// ssd_delta_chain.cu -- the gated delta rule from chunk to chunk on the tensor
-// cores: the forward recurrence of S with the outputs, and the reverse
-// recurrence of dS.  What chunks can do side by side has been done before
-// (ssd_delta_prep.cu), so that a chunk's step is, with rows p of the state on
-// the left of every product,
+// ssd_delta_chain.cu -- the gated delta rule from chunk to chunk: the forward
+// recurrence of S with the outputs, and the reverse recurrence of dS.
 //
-//   forward    E = V' - S W^T        (p x t)    U = beta E
-//              O = scale (exp(G) S Q^T + U P^T)
-//              S = exp(G_C) S + (exp(G_C - G) U)^ K
-//   backward   F = A + dS B^T        (p x t)    dv = beta F
-//              dS = exp(G_C) dS + scale (exp(G) dO)^T Q - (exp(G) beta F)^ K
+// Rows of S (one for each element of v) never mix.  A strip of 16 rows, the
+// height of a warp-level product, goes through the whole sequence with four
+// warps; its S stays in their registers as fp32 accumulators, dstate / 4
+// columns a warp.  Every product of a chunk has the strip's rows on its left
+// and tiles of the chunk (K, Q, Y, P; see ssd_delta_tiles.cuh) on its right:
 //
-// One CTA takes one head through one sequence.  The state's rows are the 128
-// lanes of tensor memory: S itself stays in registers (fp32, a row and a
-// quarter of dstate a thread, 16 warps), its fp16 goes to tensor memory as the
-// left operand, W, K, Q, P come as shared-memory tiles.  E and U likewise go
-// from the accumulator through registers back to tensor memory as a left
-// operand, so nothing that a thread computes passes through shared memory.
-// Warp 16 copies the tiles (bulk copies, two or three chunks ahead), warp 17
-// issues the products.
+//   forward    X = S K16^T                    (p x t)   R = V - exp(G) 2^a X
+//              E = R - (beta R) Y16^T 2^tau   (p x t)   U = beta 2^a E
+//              O = (exp(G) S Q16^T + U P16^T) scale 2^a
+//              S = exp(G_C) S + (U exp(G_C - G)) K16
+//   backward   dU = (exp(G_C - G) dS K16^T + scale 2^a dO P16) 2^a
+//              F = dU - (beta 2^tau dU) Y16,            dv = beta F
+//              dS = exp(G_C) dS + scale 2^a (exp(G) dO) Q16 - (exp(G) 2^a dv) K16
 //
-// What bounds the kernel is the chain of a chunk, which is sequential: product
-// with W, E and U, product with K, the new S -- about 1.4k cycles.  All that the
-// next chunk does not wait for (O, records) is issued behind it.
+// Each warp has 16 of the chunk's tokens as columns of X, R, E, O (dU, F) and
+// a quarter of dstate as columns of S, so the left operands S, R and U pass
+// through shared memory (16 rows, 2 to 4 KB) with one barrier each: three
+// barriers a chunk.  What bounds the kernel is the latency of that chain, not
+// a rate: few heads leave few strips, and every strip is sequential.  Hence
+// the smallest left operand, S in registers, and all work that the next chunk
+// does not wait for (outputs, records) behind the chain's own steps.  One warp
+// a strip, with everything in registers and no barrier, took 3.2 us a chunk
+// (2000 instructions of one warp).
 //
-// Operands are fp16 with power-of-two scales: the tiles carry theirs, S and all
-// that is in its units share one running scale a head, moved when the largest
-// value leaves [2^-2, 2^6] (by powers of 2^8; looked at one chunk late, which
-// 2^10 of head room allows).  One fp16 term is 11 bits (2^-12): enough for what
-// leaves as bf16.  Where the fp32 state itself is asked for, S, W, V' and U are
-// carried as two terms (22 bits); the sums are fp32 either way.
+// Operands are fp16 with power-of-two scales: the K, Q and Y tiles carry
+// theirs (exact for bf16 k and q), the strip's S, V, dO and all between share
+// one running scale, moved only when the largest value leaves [2^-2, 2^6].
+// One fp16 term is 11 bits (2^-12): enough for what leaves as bf16.  Where the
+// fp32 state itself is asked for, S, R, U and Y are carried as two terms (22
+// bits); k and q are exact either way, and the sums are fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "ssd_delta_tiles.cuh"
-#include "umma.cuh"
 
 namespace ssd {
 namespace delta {
 namespace {
 
-using mma16::pack;
-using mma16::pow2_inv;
-using mma16::split;
-using mma16::unpack;
+using namespace mma16;
 
-constexpr int kEpi = 16;                       // warps that hold the state
-constexpr int kThreads = 32 * (kEpi + 2);
-constexpr float kLow = 0.25f, kHigh = 64.f;    // window of the state's largest value; four times that with two terms
-constexpr uint32_t kWait = 1u << 22;           // polls before a wait gives up
-
-// Columns of tensor memory: the state's fp16 terms, accumulators, and the other left operands.
-template <int kTerms>
-struct Tmem {
-  static constexpr uint32_t kS = 0, kX = 64 * kTerms, kO = kX + 64, kW = kO + 64, kD = kW + 32 * kTerms,
-                            kO2 = kTerms == 2 ? kX : kD + 128,       // two terms leave no room: X has been read by then
-                            kU = kTerms == 2 ? kS + 64 : kD + 192;   // and S's second term has been multiplied
-  static constexpr uint32_t kAlloc = 512;
-};
-static_assert(Tmem<2>::kD + 128 <= 512 && Tmem<1>::kU + 32 <= 512, "tensor memory");
+constexpr float kLow = 0.25f, kHigh = 64.f;   // window of a strip's largest value
+constexpr int kStages = 3;    // chunks of tiles in shared memory: one worked on, two on their way
+constexpr int kRing = 4;      // chunks of v (dO) rows: the next chunk's largest value is looked at a chunk ahead
+constexpr int kBlock = kChunk * 32;   // bytes of a strip's rows: 64 tokens x 16
 
 template <int N, int kTerms>
-struct Fwd {
-  static constexpr int kTile = kChunk * N * 2;
-  static constexpr int kStages = kTerms == 2 ? 2 : 3;
-  static constexpr int kW = 0, kK = kTerms * kTile, kQ = kK + kTile, kP = kQ + kTile, kV = kP + 8192,
-                       kVecAt = kV + kTerms * kChunk * 128 * 2, kStage = kVecAt + 1024;
-};
-template <int N>
-struct Bwd {
-  static constexpr int kTile = kChunk * N * 2, kRows = kChunk * 128 * 2;
-  static constexpr int kStages = 2;
-  static constexpr int kB = 0, kK = kTile, kQ = kK + kTile, kX2 = kQ + kTile, kA = kX2 + kRows, kVecAt = kA + kRows,
-                       kStage = kVecAt + 1024;
+struct Layout {
+  static constexpr int kK = 0, kQ = kChunk * N * 2, kY = 2 * kQ, kP = kY + 8192 * kTerms, kVecAt = kP + 8192,
+                       kStage = kVecAt + (kVecChain * 4 + 127) / 128 * 128;
+  // a strip's own space: ring of v or dO, then the left operands
+  static constexpr int kS = kRing * kBlock, kR = kS + kTerms * 32 * N, kU = kR + kTerms * 2048, kW = kU + 2048,
+                       kMax = kW + kTerms * 2048, kStrip = kMax + 128;
+  __host__ __device__ static constexpr int bytes(int strips) { return kStages * kStage + strips * kStrip; }
 };
 
-// Barriers and the other words of a CTA, after the stages.
-struct Control {
-  uint64_t full[3], free[3];   // tiles of a stage have come; all that reads them is done
-  uint64_t state, left;        // the state's fp16, and the other left operands, are in tensor memory
-  uint64_t x, d, o;            // the products with W (B), K, and the outputs' are done
-  uint32_t tmem;
-  int dead;                    // a wait ran out: nothing is waited for any more
-  float top[2][kEpi];          // largest |S| of each warp, by chunk parity
+struct Chunk {
+  int64_t slot, b;   // chunk slot, first token
+  int n;             // tokens
 };
 
-struct Waits {
-  Control *c;
-  int *status;
-  __device__ __forceinline__ void operator()(uint64_t &bar, uint32_t parity) const {
-    if (*reinterpret_cast<volatile int *>(&c->dead)) return;
-    if (!umma::mbar_wait(&bar, parity & 1u, kWait)) {
-      c->dead = 1;
-      *status = 1;
+// Byte offset of 16-byte half `j` of token t in a strip's 64 x 16 block.
+__device__ __forceinline__ uint32_t row_at(int t, int j) { return t * 32 + ((j ^ ((t >> 2) & 1)) << 4); }
+// This lane's row of a transposing load or store of 16 tokens (4 matrices) of a block: accumulator layout, tokens as columns.
+__device__ __forceinline__ uint32_t block_addr(uint32_t block, int t0, int lane) {
+  return block + row_at(t0 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+}
+
+__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void strip_sync(int strip) { asm volatile("bar.sync %0, 128;" ::"r"(strip + 1) : "memory"); }
+
+// 16 x 16 values (two accumulator tiles) rounded, as the four matrices of a store.
+template <int kTerms>
+__device__ __forceinline__ void to_a(const float (&x)[4], const float (&y)[4], uint32_t (&a)[kTerms][4]) {
+  uint32_t p[kTerms];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    split<kTerms>(x[2 * i], x[2 * i + 1], p);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) a[t][i] = p[t];
+    split<kTerms>(y[2 * i], y[2 * i + 1], p);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) a[t][2 + i] = p[t];
+  }
+}
+
+// The chunk's tiles, copied by all threads of the CTA.
+template <int N, int kTerms, int kThreads>
+__device__ __forceinline__ void fetch_tiles(const Shape &s, const Tiles &t, int64_t slot, int h, uint32_t stage) {
+  using L = Layout<N, kTerms>;
+  const int tid = threadIdx.x;
+  const int64_t kt = (slot * s.G + h / s.hpg) * kChunk * N, ht = slot * s.H + h;
+  const uint8_t *K = reinterpret_cast<const uint8_t *>(t.K16 + kt) + 16 * tid;
+  const uint8_t *Q = reinterpret_cast<const uint8_t *>(t.Q16 + kt) + 16 * tid;
+  const uint8_t *Y = reinterpret_cast<const uint8_t *>(t.Y16 + ht * 2 * kTri) + 16 * tid;
+  const uint8_t *P = reinterpret_cast<const uint8_t *>(t.P16 + ht * kTri) + 16 * tid;
+  stage += 16 * tid;
+#pragma unroll
+  for (int i = 0; i < kChunk * N / 8; i += kThreads) {
+    cp16(stage + L::kK + 16 * i, K + 16 * i);
+    cp16(stage + L::kQ + 16 * i, Q + 16 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < 512 * kTerms; i += kThreads) cp16(stage + L::kY + 16 * i, Y + 16 * i);
+#pragma unroll
+  for (int i = 0; i < 512; i += kThreads) cp16(stage + L::kP + 16 * i, P + 16 * i);
+  if (tid < kVecChain / 4) cp16(stage + L::kVecAt, reinterpret_cast<const uint8_t *>(t.vec + ht * kVec) + 16 * tid);
+}
+
+// The strip's 16 columns of the chunk's v or dO, one 16-byte piece a thread; tokens past the end are zero.
+__device__ __forceinline__ void fetch_rows(const Chunk &c, const __nv_bfloat16 *x, int64_t stride, int col, bool vec,
+                                           uint32_t block, uint8_t *gblock) {
+  const int i = threadIdx.x & 127, r = i >> 1, j = i & 1;
+  const uint32_t at = row_at(r, j);
+  const __nv_bfloat16 *src = x + (c.b + r) * stride + col + 8 * j;
+  if (vec) {
+    const int n = r < c.n ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(block + at), "l"(n ? src : x), "r"(n) : "memory");
+  } else {
+    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(gblock + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dst[e] = r < c.n ? src[e] : __float2bfloat16_rn(0.f);
+  }
+}
+
+__device__ __forceinline__ void put_out(__nv_bfloat16 *p, bool vec, uint4 v) {
+  if (vec) {
+    *reinterpret_cast<uint4 *>(p) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i] & 0xffffu));
+      p[2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i] >> 16));
     }
   }
-};
+}
 
-// Factor that brings the largest value `need` back into the window (1 while it is inside, zero or not finite).  With two
-// terms the window lies higher, where the second term of a state of like elements is still a normal fp16.
-template <int kTerms>
+// This warp's 16 tokens x 16 rows through its part of `block` to [token][row]: the lane's token and half, and their 8 values.
+__device__ __forceinline__ uint4 turned(uint8_t *gblock, uint32_t block, const uint32_t (&w)[4], int t0, int lane) {
+  __syncwarp();
+  stsm4t(block_addr(block, t0, lane), w);
+  __syncwarp();
+  return *reinterpret_cast<const uint4 *>(gblock + row_at(t0 + (lane >> 1), lane & 1));
+}
+
+// Largest magnitude of a warp's bf16 pairs, as the bits of a float.
+__device__ __forceinline__ uint32_t top_of(const uint32_t (&w)[4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fff0000u, (w[i] << 16) & 0x7fff0000u));
+  return __reduce_max_sync(~0u, m);
+}
+template <int kTiles>
+__device__ __forceinline__ uint32_t top_of(const float (&S)[kTiles][4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) m = fmaxf(m, fmaxf(fmaxf(fabsf(S[i][0]), fabsf(S[i][1])), fmaxf(fabsf(S[i][2]), fabsf(S[i][3]))));
+  return __reduce_max_sync(~0u, __float_as_uint(m));
+}
+
+// Factor that brings a strip's largest value `need` back into the window (1 while it is inside, zero or not finite).
+// A power of 2^8, so that strips of like size share one scale and the gradient kernel has nothing to adjust.
 __device__ __forceinline__ float rescale(float need, float dn) {
-  if (kTerms == 2) need *= 0.25f;
   if (!(need > kHigh || (need < kLow && need > 0.f)) || isinf(need)) return 1.f;
   const int e = int(__float_as_uint(need) >> 23) - 127 + 2;   // need = 2^-2 2^e (1 to 2)
   const int k = e >= 0 ? e / 8 : (e - 7) / 8;
@@ -108,574 +176,565 @@ __device__ __forceinline__ float rescale(float need, float dn) {
   const float lim = 1.0e33f;   // keeps both scales finite
   return dn * f > lim || dn * f < 1.f / lim ? 1.f : f;
 }
-template <int n>
-__device__ __forceinline__ float warp_top(const float (&v)[n]) {
-  float m = 0.f;
+__device__ __forceinline__ float strip_top(const float *mx) {
+  const float4 v = *reinterpret_cast<const float4 *>(mx);
+  return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+}
+
+template <int kTiles>
+__device__ __forceinline__ void load_state(float (&S)[kTiles][4], const float *p, bool on, int N, int lane) {
 #pragma unroll
-  for (int i = 0; i < n; ++i) m = fmaxf(m, fabsf(v[i]));
-  return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(m)));
-}
-__device__ __forceinline__ float head_top(const float *top, int warps) {
-  float m = 0.f;
-  for (int i = 0; i < warps; ++i) m = fmaxf(m, top[i]);
-  return m;
-}
-
-__device__ __forceinline__ void epi_sync(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory"); }
-
-// Arrives when this warp's stores to tensor memory are done.
-__device__ __forceinline__ void stored(uint64_t &bar, int lane) {
-  umma::tmem_wait_st();
-  umma::fence_before_sync();
-  __syncwarp();
-  if (lane == 0) umma::mbar_arrive(&bar);
-}
-
-// 64 columns K steps of 16: descriptor of step k of a K-major panel tile [64][..], and of an MN-major one [64 = K][..].
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int k) {
-  return umma::smem_desc_sw128(tile + (k / 4) * (kChunk * 128) + (k % 4) * 32, 16, 1024);
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int k) {
-  return umma::smem_desc_sw128(tile + k * 16 * 128, kChunk * 128, 1024);
-}
-
-// Where a warp stands: rows of its tensor memory quadrant, and which quarter of the columns is its own.
-struct Place {
-  int warps;        // warps that hold rows of this head
-  int p;            // row
-  bool on, live;    // the warp has rows of the head; this thread has one
-  int quarter;
-  uint32_t lanes;   // its quadrant's lane field of a tensor memory address
-};
-__device__ __forceinline__ Place place(int P, int warp, int lane) {
-  Place l;
-  const int quads = (P + 31) / 32;
-  l.warps = 4 * quads;
-  l.p = 32 * (warp & 3) + lane;
-  l.on = warp < kEpi && (warp & 3) < quads;
-  l.live = l.on && l.p < P;
-  l.quarter = warp >> 2;
-  l.lanes = uint32_t(32 * (warp & 3)) << 16;
-  return l;
-}
-// This warp's slot among those that hold rows.
-__device__ __forceinline__ int slot_of(const Place &l, int warp) { return l.quarter * (l.warps / 4) + (warp & 3); }
-
-// The swizzled tiles need 1 KB alignment; without it nothing is done.
-__device__ __forceinline__ bool misaligned(const uint8_t *smem, int *status) {
-  if ((umma::smem_u32(smem) & 1023u) == 0) return false;
-  if (threadIdx.x == 0) *status = 2;
-  return true;
-}
-
-__device__ __forceinline__ void set_up(Control &ct, int stages, int warps, int warp, int lane, uint32_t cols) {
-  if (warp == 0) umma::tmem_alloc(&ct.tmem, cols);
-  if (warp == 1 && lane == 0) {
-    for (int i = 0; i < stages; ++i) {
-      umma::mbar_init(&ct.full[i], 1);
-      umma::mbar_init(&ct.free[i], warps);
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float2 v = on ? *reinterpret_cast<const float2 *>(p + int64_t((lane >> 2) + 8 * r) * N + 8 * i + 2 * (lane & 3))
+                          : make_float2(0.f, 0.f);
+      S[i][2 * r] = v.x;
+      S[i][2 * r + 1] = v.y;
     }
-    umma::mbar_init(&ct.state, warps);
-    umma::mbar_init(&ct.left, warps);
-    umma::mbar_init(&ct.x, 1);
-    umma::mbar_init(&ct.d, 1);
-    umma::mbar_init(&ct.o, 1);
-    umma::fence_mbar_init();
-    ct.dead = 0;
+}
+template <int kTiles>
+__device__ __forceinline__ void store_state(const float (&S)[kTiles][4], float *p, float up, int N, int lane) {
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      *reinterpret_cast<float2 *>(p + int64_t((lane >> 2) + 8 * r) * N + 8 * i + 2 * (lane & 3)) =
+          make_float2(S[i][2 * r] * up, S[i][2 * r + 1] * up);
+}
+
+__device__ __forceinline__ float2 vec2(const float *v, int i, int lane) {
+  return *reinterpret_cast<const float2 *>(v + 8 * i + 2 * (lane & 3));
+}
+
+// d (two token tiles) += left operand (16 x 16 at column k0 of `a`, rows of `ab` bytes) times 16 rows [n][k] of `tile`.
+template <int kTerms>
+__device__ __forceinline__ void mul_n(float (&d)[2][4], const uint32_t (&a)[kTerms][4], uint32_t tile, int n0, int k0,
+                                      int bytes, int lane) {
+  uint32_t b[4];
+  ldsm4(b, b_addr(tile, n0, k0, bytes, lane));
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    mma(d[0], a[t], b[0], b[1]);
+    mma(d[1], a[t], b[2], b[3]);
   }
-  umma::fence_before_sync();
-  __syncthreads();
-  umma::fence_after_sync();
 }
-// Every copy has landed before the CTA's shared memory is given up.
-__device__ __forceinline__ void drain(Control &ct, int stages, int issued) {
-  for (int c = max(0, issued - stages); c < issued; ++c) umma::mbar_wait(&ct.full[c % stages], (c / stages) & 1, kWait);
-}
-__device__ __forceinline__ void tear_down(Control &ct, int warp, uint32_t cols) {
-  umma::fence_before_sync();
-  __syncthreads();
-  if (warp == 0) {
-    umma::fence_after_sync();
-    umma::tmem_relinquish();
-    umma::tmem_dealloc(ct.tmem, cols);
+// The same, kTiles column tiles from n0, with `tile` as rows [k][n].
+template <int kTerms, int kTiles>
+__device__ __forceinline__ void mul_t(float (&d)[kTiles][4], const uint32_t (&a)[kTerms][4], uint32_t tile, int n0, int k0,
+                                      int bytes, int lane) {
+#pragma unroll
+  for (int i = 0; i < kTiles / 2; ++i) {
+    uint32_t b[4];
+    ldsm4t(b, bt_addr(tile, n0 + 16 * i, k0, bytes, lane));
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      mma(d[2 * i], a[t], b[0], b[1]);
+      mma(d[2 * i + 1], a[t], b[2], b[3]);
+    }
   }
 }
 
-// The state's fp16 terms to tensor memory; the first term is left in `hi`.
-template <int kTerms, int kCols>
-__device__ __forceinline__ void put_state(const float (&S)[kCols], uint32_t at, uint32_t (&hi)[kCols / 2]) {
-  uint32_t lo[kCols / 2];
+// The state's fp16 terms to the strip's space; called by each warp for its columns.
+template <int kTerms, int kTiles>
+__device__ __forceinline__ void put_state(const float (&S)[kTiles][4], uint32_t at, int plane, int n0, int bytes, int lane) {
 #pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) {
-    uint32_t p[kTerms];
-    split<kTerms>(S[2 * i], S[2 * i + 1], p);
-    hi[i] = p[0];
-    if (kTerms == 2) lo[i] = p[kTerms - 1];
+  for (int i = 0; i < kTiles / 2; ++i) {
+    uint32_t a[kTerms][4];
+    to_a<kTerms>(S[2 * i], S[2 * i + 1], a);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) stsm4(a_addr(at + t * plane, 0, n0 + 16 * i, bytes, lane), a[t]);
   }
-  umma::tmem_st(at, hi);
-  if (kTerms == 2) umma::tmem_st(at + 64, lo);
-}
-// This thread's part of the fp16 state's row p to the record: 16-byte chunks j0.. of a panel tile of P rows.
-template <int kWords>
-__device__ __forceinline__ void save_state(const uint32_t (&hi)[kWords], __half *tile, int p, int j0, int P) {
-  uint8_t *to = reinterpret_cast<uint8_t *>(tile);
-#pragma unroll
-  for (int i = 0; i < kWords / 4; ++i)
-    *reinterpret_cast<uint4 *>(to + pan(p, j0 + i, P)) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-}
-template <int kCols>
-__device__ __forceinline__ void load_d(uint32_t at, float (&v)[kCols]) {
-  if constexpr (kCols == 32) umma::tmem_ld32(at, v);
-  else umma::tmem_ld16(at, v);
 }
 
-// CTA (head, sequence).
-template <int N, int kTerms, bool kSave>
-__global__ void __launch_bounds__(kThreads, 1) chain_fwd_kernel(Shape s, Args a, Tiles t) {
-  using L = Fwd<N, kTerms>;
-  using M = Tmem<kTerms>;
-  constexpr int kCols = N / 4, kStages = L::kStages;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Control &ct = *reinterpret_cast<Control *>(smem + kStages * L::kStage);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x;
-  const int64_t seq = blockIdx.y;
-  const Place me = place(s.P, warp, lane);
-  const Waits wait{&ct, t.status};
-  if (misaligned(smem, t.status)) return;
-  set_up(ct, kStages, me.warps, warp, lane, M::kAlloc);
-  const uint32_t base = umma::smem_u32(smem), tm = ct.tmem;
+// CTA (kStrips strips of 16 rows, head, sequence), four warps a strip.
+template <int N, int kTerms, int kStrips, bool kSave>
+__global__ void __launch_bounds__(128 * kStrips) chain_fwd_kernel(Shape s, Args a, Tiles t, int vvec, int ovec) {
+  using L = Layout<N, kTerms>;
+  constexpr int kTiles = N / 32, NB = 2 * N, kPlane = 32 * N;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
+  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * 16, n0 = w * (N / 4), t0w = 16 * w;
+  const bool live = p0 < s.P;
+  const int64_t seq = blockIdx.z;
   int64_t t0, te;
   seq_range(s, a.cu, seq, t0, te);
-  const int64_t slot0 = first_slot(s, a.cu, seq, t0);
-  const int nc = int(min((te - t0 + kChunk - 1) / kChunk, s.slots - slot0));
-
-  if (warp == kEpi) {   // copies
-    if (lane == 0) {
-      int issued = 0;
-      const uint32_t vbytes = uint32_t(kTerms * kChunk * s.P * 2);
-      for (int c = 0; c < nc; ++c) {
-        const int st = c % kStages;
-        if (c >= kStages) wait(ct.free[st], c / kStages - 1);
-        if (*reinterpret_cast<volatile int *>(&ct.dead)) break;
-        uint8_t *to = smem + st * L::kStage;
-        const int64_t ht = (slot0 + c) * s.H + h, kt = ((slot0 + c) * s.G + h / s.hpg) * kChunk * N;
-        umma::mbar_expect_tx(&ct.full[st], (kTerms + 2) * L::kTile + 8192 + vbytes + kVecChain * 4);
-        umma::bulk_load(to + L::kW, t.W16 + ht * kTerms * kChunk * N, kTerms * L::kTile, &ct.full[st]);
-        umma::bulk_load(to + L::kK, t.K16 + kt, L::kTile, &ct.full[st]);
-        umma::bulk_load(to + L::kQ, t.Q16 + kt, L::kTile, &ct.full[st]);
-        umma::bulk_load(to + L::kP, t.P16 + ht * kTri, 8192, &ct.full[st]);
-        umma::bulk_load(to + L::kV, t.V16 + ht * kTerms * kChunk * s.P, vbytes, &ct.full[st]);
-        umma::bulk_load(to + L::kVecAt, t.vec + ht * kVec, kVecChain * 4, &ct.full[st]);
-        issued = c + 1;
-      }
-      drain(ct, kStages, issued);
+  const int64_t slot0 = first_slot(s, a.cu, seq, t0), nc = (te - t0 + kChunk - 1) / kChunk;
+  const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v);
+  __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
+  const uint32_t base = smem_at(smem), own = base + kStages * L::kStage + strip * L::kStrip;
+  uint8_t *gown = smem + kStages * L::kStage + strip * L::kStrip;
+  float *mx = reinterpret_cast<float *>(gown + L::kMax);
+  auto chunk = [&](int64_t c) {
+    return Chunk{min(slot0 + c, s.slots - 1), t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
+  };
+  auto fetch_v = [&](int64_t c) {
+    if (c < nc && live) {
+      const int at = int(c % kRing) * kBlock;
+      fetch_rows(chunk(c), v, s.vs, h * s.P + p0, vvec, own + at, gown + at);
     }
-    __syncwarp();
-  } else if (warp == kEpi + 1) {   // products
-    if (lane == 0) {
-      constexpr uint32_t to_t = umma::idesc_f16_f32(128, kChunk, 0, 0);   // columns t: tiles [t][k]
-      constexpr uint32_t to_n = umma::idesc_f16_f32(128, N, 0, 1);        // columns n: tiles [t = k][n]
-      for (int c = 0; c < nc; ++c) {
-        const int st = c % kStages;
-        const uint32_t tile = base + st * L::kStage;
-        wait(ct.full[st], c / kStages);
-        wait(ct.state, c);
-        if (kTerms == 2 && c > 0) wait(ct.free[(c - 1) % kStages], (c - 1) / kStages);   // O has been read out of X's columns
-        umma::fence_after_sync();
+  };
+  auto fetch = [&](int64_t c) {   // the tiles of chunk c and the rows of the one after
+    if (c < nc) fetch_tiles<N, kTerms, 128 * kStrips>(s, t, chunk(c).slot, h, base + int(c % kStages) * L::kStage);
+    fetch_v(c + 1);
+    cp_commit();
+  };
+  float S[kTiles][4], up = 1.f, dn = 1.f;
+  const int64_t row = ((seq * s.H + h) * s.P + p0) * N + n0;
+  load_state<kTiles>(S, a.init + row, live && a.init != nullptr, N, lane);
+  fetch_v(0);
+  cp_commit();
+  fetch(0);
+  fetch(1);
+  // v of chunk c, this warp's tokens, as packed pairs
+  auto load_v = [&](uint32_t (&x)[4], int64_t c) { ldsm4t(x, block_addr(own + int(c % kRing) * kBlock, t0w, lane)); };
+  auto move = [&](float f) {
+    if (f != 1.f) {
 #pragma unroll
-        for (int x = 0; x < (kTerms == 2 ? 3 : 1); ++x)   // S W, then S's second term, then W's
+      for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-          for (int k = 0; k < N / 16; ++k)
-            umma::mma_f16_ta(tm + M::kX, tm + M::kS + (x == 1 ? 64 : 0) + 8 * k,
-                             desc_k(tile + L::kW + (x == 2 ? L::kTile : 0), k), to_t, x + k > 0);
-        umma::mma_commit(&ct.x);
-        if (kTerms == 1 && c > 0) wait(ct.free[(c - 1) % kStages], (c - 1) / kStages);
-#pragma unroll
-        for (int k = 0; k < N / 16; ++k)
-          umma::mma_f16_ta(tm + M::kO, tm + M::kS + 8 * k, desc_k(tile + L::kQ, k), to_t, k > 0);
-        wait(ct.left, c);
-        umma::fence_after_sync();
-        auto outputs = [&]() {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma::mma_f16_ta(tm + M::kO2, tm + M::kU + 8 * k, desc_k(tile + L::kP, k), to_t, k > 0);
-        };
-        if (kTerms == 2) outputs();   // its left operand lies where the new state will
-#pragma unroll
-        for (int x = 0; x < kTerms; ++x)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma::mma_f16_ta(tm + M::kD, tm + M::kW + 32 * x + 8 * k, desc_mn(tile + L::kK, k), to_n, x + k > 0);
-        umma::mma_commit(&ct.d);
-        if (kTerms == 1) {
-          outputs();
-          umma::mma_commit(&ct.o);
-        }
-      }
+        for (int r = 0; r < 4; ++r) S[i][r] *= f;
+      dn *= f;
+      up *= pow2_inv(f);
     }
-    __syncwarp();
-  } else if (me.on) {
-    const int my = slot_of(me, warp), P = s.P, n0 = kCols * me.quarter, tq = 16 * me.quarter;
-    const uint32_t lanes = tm + me.lanes;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + int64_t(h) * P + me.p;
-    const int64_t row = ((seq * s.H + h) * P + me.p) * N + n0;
-    float S[kCols], up = 1.f, dn = 1.f;
-#pragma unroll
-    for (int i = 0; i < kCols; i += 4) {
-      const float4 v = me.live && a.init != nullptr ? *reinterpret_cast<const float4 *>(a.init + row + i)
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
-    }
-    // V's largest value is below 16 times its tile's scale
-    auto incoming = [&](int c) { return c < nc ? 16.f * __ldg(t.vec + ((slot0 + c) * s.H + h) * kVec + kVecSv) : 0.f; };
-    auto move = [&](float f) {
-      if (f != 1.f) {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) S[i] *= f;
-        dn *= f;
-        up *= pow2_inv(f);
-      }
-    };
-    // the state entering chunk c: to tensor memory, and to the record behind it
-    auto enter = [&](int c) {
-      uint32_t hi[kCols / 2];
-      put_state<kTerms, kCols>(S, lanes + M::kS + n0 / 2, hi);
-      const float m = warp_top(S);
-      if (lane == 0) ct.top[c & 1][my] = m;
-      stored(ct.state, lane);
-      if (kSave) {
-        const int64_t ht = (slot0 + c) * s.H + h;
-        if (me.live) save_state(hi, t.S16 + ht * P * N, me.p, n0 / 8, P);
-        if (my == 0 && lane == 0) t.up[ht] = up;
-      }
-    };
-    if (nc > 0) {
-      const float m = warp_top(S);
-      if (lane == 0) ct.top[1][my] = m;
-      epi_sync(me.warps);
-      move(rescale<kTerms>(fmaxf(head_top(ct.top[1], me.warps), incoming(0)), 1.f));
-      enter(0);
-    }
-    for (int c = 0; c < nc; ++c) {
-      const int st = c % kStages;
-      const uint8_t *tile = smem + st * L::kStage;
-      const float *vec = reinterpret_cast<const float *>(tile + L::kVecAt);
-      const __half *V = reinterpret_cast<const __half *>(tile + L::kV);
-      const int64_t ht = (slot0 + c) * s.H + h, b = t0 + int64_t(c) * kChunk;
-      const int n = int(min(int64_t(kChunk), te - b));
-      const float next = incoming(c + 1);
-      wait(ct.full[st], c / kStages);
-      const float ka = vec[kVecKa], sv = vec[kVecSv] * dn, last = vec[kVecEg + kChunk - 1];
-      float E[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x = 0.f;
-        if (me.live) {
-          x = __half2float(V[(tq + i) * P + me.p]);
-          if (kTerms == 2) x += __half2float(V[(kChunk + tq + i) * P + me.p]);
-        }
-        E[i] = x * sv;
-      }
-      wait(ct.x, c);
-      umma::fence_after_sync();
-      uint32_t e16[8];
-      {
-        float X[16];
-        umma::tmem_ld16(lanes + M::kX + tq, X);
-        uint32_t u[8], w0[8], w1[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 tl = *reinterpret_cast<const float2 *>(vec + kVecTail + tq + 2 * i);
-          const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta + tq + 2 * i);
-          const float e0 = fmaf(-ka, X[2 * i], E[2 * i]), e1 = fmaf(-ka, X[2 * i + 1], E[2 * i + 1]);
-          if (kSave) e16[i] = pack(e0, e1);
-          const float u0 = e0 * be.x, u1 = e1 * be.y;
-          u[i] = pack(u0, u1);
-          uint32_t p[kTerms];
-          split<kTerms>(u0 * tl.x, u1 * tl.y, p);
-          w0[i] = p[0];
-          w1[i] = p[kTerms - 1];
-        }
-        umma::tmem_st(lanes + M::kW + tq / 2, w0);
-        if (kTerms == 2) umma::tmem_st(lanes + M::kW + 32 + tq / 2, w1);
-        umma::tmem_st(lanes + M::kU + tq / 2, u);
-        stored(ct.left, lane);
-      }
-      wait(ct.state, c);   // over long since: makes the other warps' `top` visible
-      const float f = c + 1 < nc ? rescale<kTerms>(fmaxf(head_top(ct.top[c & 1], me.warps), next * dn), dn) : 1.f;
-      if (kSave && me.live) {
-        __half *e = t.E16 + (ht * kChunk + tq) * P + me.p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const __half2 v = *reinterpret_cast<const __half2 *>(&e16[i]);
-          e[2 * i * P] = __low2half(v);
-          e[(2 * i + 1) * P] = __high2half(v);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) S[i] *= last;
-      const float co = a.scale * ka * up;
-      float O[16];
-      auto outputs = [&]() {
-        float o2[16];
-        umma::tmem_ld16(lanes + M::kO + tq, O);
-        umma::tmem_ld16(lanes + M::kO2 + tq, o2);
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float2 eg = *reinterpret_cast<const float2 *>(vec + kVecEg + tq + i);
-          O[i] = co * fmaf(eg.x, O[i], ka * o2[i]);
-          O[i + 1] = co * fmaf(eg.y, O[i + 1], ka * o2[i + 1]);
-        }
-        umma::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&ct.free[st]);
-      };
-      wait(ct.d, c);
-      umma::fence_after_sync();
-      if (kTerms == 2) outputs();   // before X's columns are written again
-      {
-        float D[kCols];
-        load_d(lanes + M::kD + n0, D);
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) S[i] = me.live ? fmaf(ka, D[i], S[i]) : 0.f;
-      }
-      move(f);
-      if (c + 1 < nc) enter(c + 1);
-      if (kTerms == 1) {
-        wait(ct.o, c);
-        umma::fence_after_sync();
-        outputs();
-      }
-      if (me.live) {
-        __nv_bfloat16 *to = o + (b + tq) * s.H * P;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (tq + i < n) to[int64_t(i) * s.H * P] = __float2bfloat16_rn(O[i]);
-      }
-    }
-    if (me.live && a.fin != nullptr) {
-#pragma unroll
-      for (int i = 0; i < kCols; i += 4)
-        *reinterpret_cast<float4 *>(a.fin + row + i) = make_float4(S[i] * up, S[i + 1] * up, S[i + 2] * up, S[i + 3] * up);
+  };
+  if (nc > 0) {
+    cp_wait<2>();
+    __syncthreads();
+    if (live) {
+      uint32_t x[4];
+      load_v(x, 0);
+      const float m = fmaxf(__uint_as_float(top_of(x)), __uint_as_float(top_of<kTiles>(S)));
+      if (lane == 0) mx[4 + w] = m;
+      strip_sync(strip);
+      move(rescale(strip_top(mx + 4), 1.f));
     }
   }
-  tear_down(ct, warp, M::kAlloc);
+  for (int64_t c = 0; c < nc; ++c) {
+    if (live) put_state<kTerms, kTiles>(S, own + L::kS, kPlane, n0, NB, lane);
+    cp_wait<1>();
+    __syncthreads();   // tiles of c, rows of c + 1, S of every warp; everyone is done with chunk c - 1
+    fetch(c + 2);
+    if (!live) continue;
+    const Chunk ck = chunk(c);
+    const int64_t ht = ck.slot * s.H + h;
+    const int stage = int(c % kStages) * L::kStage, ring = int(c % kRing) * kBlock;
+    const uint32_t ks = base + stage + L::kK, qs = base + stage + L::kQ, ys = base + stage + L::kY, ps = base + stage + L::kP;
+    const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
+    const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1];
+    const float2 eg[2] = {vec2(vec + kVecEg + t0w, 0, lane), vec2(vec + kVecEg + t0w, 1, lane)};
+    uint32_t vw[4];
+    load_v(vw, c);
+    float R[2][4] = {}, O[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < N / 16; ++j) {
+      uint32_t sa[kTerms][4], one[1][4];
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) ldsm4(sa[i], a_addr(own + L::kS + i * kPlane, 0, 16 * j, NB, lane));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) one[0][i] = sa[0][i];
+      mul_n<kTerms>(R, sa, ks, t0w, 16 * j, NB, lane);
+      mul_n<1>(O, one, qs, t0w, 16 * j, NB, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 v0 = unpack_bf16(vw[2 * i]), v1 = unpack_bf16(vw[2 * i + 1]);
+      const float c0 = eg[i].x * ka, c1 = eg[i].y * ka;
+      R[i][0] = fmaf(-c0, R[i][0], v0.x * dn);
+      R[i][1] = fmaf(-c1, R[i][1], v0.y * dn);
+      R[i][2] = fmaf(-c0, R[i][2], v1.x * dn);
+      R[i][3] = fmaf(-c1, R[i][3], v1.y * dn);
+    }
+    float2 be[2];
+    {
+      float B[2][4];
+      uint32_t ra[kTerms][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        be[i] = vec2(vec + kVecBeta + t0w, i, lane);
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          B[i][r] = R[i][r] * be[i].x;
+          B[i][r + 1] = R[i][r + 1] * be[i].y;
+        }
+      }
+      to_a<kTerms>(B[0], B[1], ra);
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) stsm4(a_addr(own + L::kR + 2048 * i, 0, t0w, 128, lane), ra[i]);
+    }
+    strip_sync(strip);
+    float E[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= w) {
+        uint32_t ra[kTerms][4];
+#pragma unroll
+        for (int i = 0; i < kTerms; ++i) ldsm4(ra[i], a_addr(own + L::kR + 2048 * i, 0, 16 * j, 128, lane));
+        mul_n<kTerms>(E, ra, ys, t0w, 16 * j, 128, lane);
+        if constexpr (kTerms == 2) {
+          uint32_t one[1][4] = {{ra[0][0], ra[0][1], ra[0][2], ra[0][3]}};
+          mul_n<1>(E, one, ys + 8192, t0w, 16 * j, 128, lane);
+        }
+      }
+    float W[2][4];
+    uint32_t ew[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 tau = vec2(vec + kVecTau + t0w, i, lane), tl = vec2(vec + kVecTail + t0w, i, lane);
+      const float c0 = be[i].x * ka, c1 = be[i].y * ka;
+#pragma unroll
+      for (int r = 0; r < 4; r += 2) {
+        const float e0 = fmaf(-tau.x, E[i][r], R[i][r]), e1 = fmaf(-tau.y, E[i][r + 1], R[i][r + 1]);
+        if (kSave) ew[2 * i + r / 2] = pack(e0, e1);
+        E[i][r] = e0 * c0;
+        E[i][r + 1] = e1 * c1;
+        W[i][r] = E[i][r] * tl.x;
+        W[i][r + 1] = E[i][r + 1] * tl.y;
+      }
+    }
+    {
+      uint32_t ua[1][4], wa[kTerms][4];
+      to_a<kTerms>(W[0], W[1], wa);
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) stsm4(a_addr(own + L::kW + 2048 * i, 0, t0w, 128, lane), wa[i]);
+      to_a<1>(E[0], E[1], ua);
+      stsm4(a_addr(own + L::kU, 0, t0w, 128, lane), ua[0]);
+    }
+    {
+      // the next chunk's scale: its rows, and this chunk's state (which one chunk cannot carry out of fp16's range)
+      uint32_t x[4] = {0, 0, 0, 0};
+      if (c + 1 < nc) load_v(x, c + 1);
+      const float m = fmaxf(__uint_as_float(top_of(x)) * dn, __uint_as_float(top_of<kTiles>(S)));
+      if (lane == 0) mx[4 * (c & 1) + w] = m;
+    }
+    if (kSave) {
+      // the state entering the chunk as it stands in shared memory: 16 rows, contiguous in the record
+      uint8_t *to = reinterpret_cast<uint8_t *>(t.S16 + (ht * s.P + p0) * N);
+#pragma unroll
+      for (int i = 0; i < 2 * N; i += 128) {
+        const int at = 16 * (i + (threadIdx.x & 127));
+        *reinterpret_cast<uint4 *>(to + at) = *reinterpret_cast<const uint4 *>(gown + L::kS + at);
+      }
+      if ((threadIdx.x & 127) == 0) t.up[(ht * s.P + p0) >> 4] = up;
+    }
+    strip_sync(strip);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] *= last;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t wa[kTerms][4];
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) ldsm4(wa[i], a_addr(own + L::kW + 2048 * i, 0, 16 * j, 128, lane));
+      mul_t<kTerms, kTiles>(S, wa, ks, n0, 16 * j, NB, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; r += 2) {
+        O[i][r] *= eg[i].x;
+        O[i][r + 1] *= eg[i].y;
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= w) {
+        uint32_t ua[1][4];
+        ldsm4(ua[0], a_addr(own + L::kU, 0, 16 * j, 128, lane));
+        mul_n<1>(O, ua, ps, t0w, 16 * j, 128, lane);
+      }
+    // outputs and record through this warp's tokens of the v block, which it alone has read
+    const int tok = t0w + (lane >> 1);
+    const float co = a.scale * ka * up;
+    uint32_t ow[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ow[2 * i] = pack_bf16(O[i][0] * co, O[i][1] * co);
+      ow[2 * i + 1] = pack_bf16(O[i][2] * co, O[i][3] * co);
+    }
+    const uint4 ov = turned(gown + ring, own + ring, ow, t0w, lane);
+    if (tok < ck.n) put_out(o + ((ck.b + tok) * s.H + h) * s.P + p0 + 8 * (lane & 1), ovec, ov);
+    if (kSave)
+      *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + tok) * s.P + p0 + 8 * (lane & 1)) =
+          turned(gown + ring, own + ring, ew, t0w, lane);
+    move(rescale(strip_top(mx + 4 * (c & 1)), dn));
+  }
+  cp_wait<0>();
+  if (live && a.fin != nullptr) store_state<kTiles>(S, a.fin + row, up, N, lane);
 }
 
-// The reverse recurrence; writes dv, dinit, and for the gradient kernel dS leaving each chunk (D16) and F (F16).
-template <int N>
-__global__ void __launch_bounds__(kThreads, 1) chain_bwd_kernel(Shape s, Args a, Tiles t, BwdTiles o) {
-  using L = Bwd<N>;
-  constexpr int kCols = N / 4, kStages = L::kStages;
-  // columns: dS's fp16, F, the left operand of K, and the two terms of the change of dS
-  constexpr uint32_t kS = 0, kX = 64, kW = 128, kD = 160, kD2 = 288, kAlloc = 512;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Control &ct = *reinterpret_cast<Control *>(smem + kStages * L::kStage);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x;
-  const int64_t seq = blockIdx.y;
-  const Place me = place(s.P, warp, lane);
-  const Waits wait{&ct, o.status};
-  if (misaligned(smem, o.status)) return;
-  set_up(ct, kStages, me.warps, warp, lane, kAlloc);
-  const uint32_t base = umma::smem_u32(smem), tm = ct.tmem;
+// The reverse recurrence; writes dv, dinit, and for the gradient kernel dS leaving each chunk (D16), F (F16) and dO (X16).
+template <int N, int kStrips>
+__global__ void __launch_bounds__(128 * kStrips) chain_bwd_kernel(Shape s, Args a, Tiles t, BwdTiles o, int gvec, int ovec) {
+  using L = Layout<N, 1>;
+  constexpr int kTiles = N / 32, NB = 2 * N;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
+  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * 16, n0 = w * (N / 4), t0w = 16 * w;
+  const bool live = p0 < s.P;
+  const int64_t seq = blockIdx.z, tok_stride = int64_t(s.H) * s.P;
   int64_t t0, te;
   seq_range(s, a.cu, seq, t0, te);
-  const int64_t slot0 = first_slot(s, a.cu, seq, t0);
-  const int nc = int(min((te - t0 + kChunk - 1) / kChunk, s.slots - slot0));
-  auto slot_at = [&](int c) { return slot0 + nc - 1 - c; };   // step c takes the sequence's chunk nc - 1 - c
-
-  if (warp == kEpi) {
-    if (lane == 0) {
-      int issued = 0;
-      const uint32_t abytes = uint32_t(kChunk * s.P * 2), xbytes = uint32_t(kChunk * padded(s.P) * 2);
-      for (int c = 0; c < nc; ++c) {
-        const int st = c % kStages;
-        if (c >= kStages) wait(ct.free[st], c / kStages - 1);
-        if (*reinterpret_cast<volatile int *>(&ct.dead)) break;
-        uint8_t *to = smem + st * L::kStage;
-        const int64_t ht = slot_at(c) * s.H + h, kt = (slot_at(c) * s.G + h / s.hpg) * kChunk * N;
-        umma::mbar_expect_tx(&ct.full[st], 3 * L::kTile + abytes + xbytes + kVecChain * 4 + kSide * 4);
-        umma::bulk_load(to + L::kB, o.B16 + ht * kChunk * N, L::kTile, &ct.full[st]);
-        umma::bulk_load(to + L::kK, t.K16 + kt, L::kTile, &ct.full[st]);
-        umma::bulk_load(to + L::kQ, t.Q16 + kt, L::kTile, &ct.full[st]);
-        umma::bulk_load(to + L::kX2, o.X2 + ht * kChunk * padded(s.P), xbytes, &ct.full[st]);
-        umma::bulk_load(to + L::kA, o.A16 + ht * kChunk * s.P, abytes, &ct.full[st]);
-        umma::bulk_load(to + L::kVecAt, t.vec + ht * kVec, kVecChain * 4, &ct.full[st]);
-        umma::bulk_load(to + L::kVecAt + kVecChain * 4, o.side + ht * kSide, kSide * 4, &ct.full[st]);
-        issued = c + 1;
-      }
-      drain(ct, kStages, issued);
+  const int64_t slot0 = first_slot(s, a.cu, seq, t0), nc = (te - t0 + kChunk - 1) / kChunk;
+  const __nv_bfloat16 *go = static_cast<const __nv_bfloat16 *>(a.dout);
+  __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv);
+  const uint32_t base = smem_at(smem), own = base + kStages * L::kStage + strip * L::kStrip;
+  uint8_t *gown = smem + kStages * L::kStage + strip * L::kStrip;
+  float *mx = reinterpret_cast<float *>(gown + L::kMax);
+  // step i of the sweep takes chunk nc - 1 - i of the sequence
+  auto chunk = [&](int64_t i) {
+    const int64_t c = nc - 1 - i;
+    return Chunk{min(slot0 + c, s.slots - 1), t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
+  };
+  auto fetch_x = [&](int64_t c) {
+    if (c < nc && live) {
+      const int at = int(c % kRing) * kBlock;
+      fetch_rows(chunk(c), go, tok_stride, h * s.P + p0, gvec, own + at, gown + at);
     }
-    __syncwarp();
-  } else if (warp == kEpi + 1) {
-    if (lane == 0) {
-      constexpr uint32_t to_t = umma::idesc_f16_f32(128, kChunk, 0, 0);
-      constexpr uint32_t to_n = umma::idesc_f16_f32(128, N, 0, 1);
-      constexpr uint32_t from_x = umma::idesc_f16_f32(128, N, 1, 1);   // left operand: tile [t = k][p]
-      for (int c = 0; c < nc; ++c) {
-        const int st = c % kStages;
-        const uint32_t tile = base + st * L::kStage;
-        wait(ct.full[st], c / kStages);
-        wait(ct.state, c);
-        umma::fence_after_sync();
+  };
+  auto fetch = [&](int64_t c) {
+    if (c < nc) fetch_tiles<N, 1, 128 * kStrips>(s, t, chunk(c).slot, h, base + int(c % kStages) * L::kStage);
+    fetch_x(c + 1);
+    cp_commit();
+  };
+  float D[kTiles][4], up = 1.f, dn = 1.f;
+  const int64_t row = ((seq * s.H + h) * s.P + p0) * N + n0;
+  load_state<kTiles>(D, a.dfinal + row, live && a.dfinal != nullptr, N, lane);
+  fetch_x(0);
+  cp_commit();
+  fetch(0);
+  fetch(1);
+  // dO of this warp's tokens in units of the strip's scale; its fp16 takes the place of dO in the ring
+  float X[2][4];
+  auto take_x = [&](const uint32_t (&x)[4], int64_t c) {
 #pragma unroll
-        for (int k = 0; k < N / 16; ++k)
-          umma::mma_f16_ta(tm + kX, tm + kS + 8 * k, desc_k(tile + L::kB, k), to_t, k > 0);
-        umma::mma_commit(&ct.x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma::mma_f16(tm + kD2, desc_mn(tile + L::kX2, k), desc_mn(tile + L::kQ, k), from_x, k > 0);
-        wait(ct.left, c);
-        umma::fence_after_sync();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma::mma_f16_ta(tm + kD, tm + kW + 8 * k, desc_mn(tile + L::kK, k), to_n, k > 0);
-        umma::mma_commit(&ct.d);
-      }
+    for (int i = 0; i < 2; ++i) {
+      const float2 v0 = unpack_bf16(x[2 * i]), v1 = unpack_bf16(x[2 * i + 1]);
+      X[i][0] = v0.x * dn;
+      X[i][1] = v0.y * dn;
+      X[i][2] = v1.x * dn;
+      X[i][3] = v1.y * dn;
     }
-    __syncwarp();
-  } else if (me.on) {
-    const int my = slot_of(me, warp), P = s.P, n0 = kCols * me.quarter, tq = 16 * me.quarter;
-    const uint32_t lanes = tm + me.lanes;
-    __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv) + int64_t(h) * P + me.p;
-    const int64_t row = ((seq * s.H + h) * P + me.p) * N + n0;
-    float D[kCols], up = 1.f, dn = 1.f;
+    uint32_t xa[1][4];
+    to_a<1>(X[0], X[1], xa);
+    stsm4t(block_addr(own + int(c % kRing) * kBlock, t0w, lane), xa[0]);
+  };
+  auto load_x = [&](uint32_t (&x)[4], int64_t c) { ldsm4t(x, block_addr(own + int(c % kRing) * kBlock, t0w, lane)); };
+  auto move = [&](float f) {
+    if (f != 1.f) {
 #pragma unroll
-    for (int i = 0; i < kCols; i += 4) {
-      const float4 v = me.live && a.dfinal != nullptr ? *reinterpret_cast<const float4 *>(a.dfinal + row + i)
-                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-      D[i] = v.x, D[i + 1] = v.y, D[i + 2] = v.z, D[i + 3] = v.w;
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) D[i][r] *= f;
+      dn *= f;
+      up *= pow2_inv(f);
     }
-    // A's largest value is below 16 times its tile's scale
-    auto incoming = [&](int c) { return c < nc ? 16.f * fabsf(__ldg(o.side + (slot_at(c) * s.H + h) * kSide)) : 0.f; };
-    auto move = [&](float f) {
-      if (f != 1.f) {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) D[i] *= f;
-        dn *= f;
-        up *= pow2_inv(f);
-      }
-    };
-    // the gradient of the state leaving the chunk of step c: to tensor memory, and to the record behind it
-    auto leave = [&](int c) {
-      uint32_t hi[kCols / 2];
-      put_state<1, kCols>(D, lanes + kS + n0 / 2, hi);
-      const float m = warp_top(D);
-      if (lane == 0) ct.top[c & 1][my] = m;
-      stored(ct.state, lane);
-      const int64_t ht = slot_at(c) * s.H + h;
-      if (me.live) save_state(hi, o.D16 + ht * P * N, me.p, n0 / 8, P);
-      if (my == 0 && lane == 0) o.ub[ht] = up;
-    };
-    if (nc > 0) {
-      const float m = warp_top(D);
-      if (lane == 0) ct.top[1][my] = m;
-      epi_sync(me.warps);
-      move(rescale<1>(fmaxf(head_top(ct.top[1], me.warps), incoming(0)), 1.f));
-      leave(0);
-    }
-    for (int c = 0; c < nc; ++c) {
-      const int st = c % kStages;
-      const uint8_t *tile = smem + st * L::kStage;
-      const float *vec = reinterpret_cast<const float *>(tile + L::kVecAt);
-      const __half *A = reinterpret_cast<const __half *>(tile + L::kA);
-      const int64_t ht = slot_at(c) * s.H + h, b = t0 + int64_t(nc - 1 - c) * kChunk;
-      const int n = int(min(int64_t(kChunk), te - b));
-      const float next = incoming(c + 1);
-      wait(ct.full[st], c / kStages);
-      const float ka = vec[kVecKa], sa = vec[kVecChain] * dn, sx = vec[kVecChain + 1] * dn, last = vec[kVecEg + kChunk - 1];
-      float F[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) F[i] = me.live ? sa * __half2float(A[(tq + i) * P + me.p]) : 0.f;
-      wait(ct.x, c);
-      umma::fence_after_sync();
-      {
-        float X[16];
-        umma::tmem_ld16(lanes + kX + tq, X);
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 eg = *reinterpret_cast<const float2 *>(vec + kVecEg + tq + 2 * i);
-          const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta + tq + 2 * i);
-          F[2 * i] = fmaf(ka, X[2 * i], F[2 * i]);
-          F[2 * i + 1] = fmaf(ka, X[2 * i + 1], F[2 * i + 1]);
-          w[i] = pack(F[2 * i] * (-ka * eg.x * be.x), F[2 * i + 1] * (-ka * eg.y * be.y));
-        }
-        umma::tmem_st(lanes + kW + tq / 2, w);
-        stored(ct.left, lane);
-      }
-      wait(ct.state, c);   // over long since: makes the other warps' `top` visible
-      const float f = c + 1 < nc ? rescale<1>(fmaxf(head_top(ct.top[c & 1], me.warps), next * dn), dn) : 1.f;
-      if (me.live) {
-        __nv_bfloat16 *to = dv + (b + tq) * s.H * P;
-        __half *f16 = o.F16 + (ht * kChunk + tq) * P + me.p;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          f16[i * P] = __float2half_rn(F[i]);
-          if (tq + i < n) to[int64_t(i) * s.H * P] = __float2bfloat16_rn(F[i] * (vec[kVecBeta + tq + i] * up));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) D[i] *= last;
-      const float co = a.scale * ka * sx;
-      wait(ct.d, c);
-      umma::fence_after_sync();
-      {
-        float d[kCols];
-        load_d(lanes + kD2 + n0, d);
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) D[i] = fmaf(co, d[i], D[i]);
-        load_d(lanes + kD + n0, d);
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) D[i] = me.live ? D[i] + d[i] : 0.f;   // lanes past the head hold anything
-      }
-      move(f);
-      umma::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) umma::mbar_arrive(&ct.free[st]);
-      if (c + 1 < nc) leave(c + 1);
-    }
-    if (me.live && a.dinit != nullptr) {
-#pragma unroll
-      for (int i = 0; i < kCols; i += 4)
-        *reinterpret_cast<float4 *>(a.dinit + row + i) = make_float4(D[i] * up, D[i + 1] * up, D[i + 2] * up, D[i + 3] * up);
+  };
+  if (nc > 0) {
+    cp_wait<2>();
+    __syncthreads();
+    if (live) {
+      uint32_t x[4];
+      load_x(x, 0);
+      const float m = fmaxf(__uint_as_float(top_of(x)), __uint_as_float(top_of<kTiles>(D)));
+      if (lane == 0) mx[4 + w] = m;
+      strip_sync(strip);
+      move(rescale(strip_top(mx + 4), 1.f));
+      take_x(x, 0);
     }
   }
-  tear_down(ct, warp, kAlloc);
+  for (int64_t c = 0; c < nc; ++c) {
+    if (live) put_state<1, kTiles>(D, own + L::kS, 0, n0, NB, lane);
+    cp_wait<1>();
+    __syncthreads();   // tiles of c, rows of c + 1, dS and dO of every warp; everyone is done with chunk c - 1
+    fetch(c + 2);
+    if (!live) continue;
+    const Chunk ck = chunk(c);
+    const int64_t ht = ck.slot * s.H + h;
+    const int stage = int(c % kStages) * L::kStage, ring = int(c % kRing) * kBlock;
+    const uint32_t ks = base + stage + L::kK, qs = base + stage + L::kQ, ys = base + stage + L::kY, ps = base + stage + L::kP;
+    const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
+    const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1], co = a.scale * ka;
+    float F[2][4] = {}, A[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < N / 16; ++j) {
+      uint32_t da[1][4];
+      ldsm4(da[0], a_addr(own + L::kS, 0, 16 * j, NB, lane));
+      mul_n<1>(F, da, ks, t0w, 16 * j, NB, lane);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j >= w) {
+        uint32_t xa[1][4];
+        ldsm4t(xa[0], block_addr(own + ring, 16 * j, lane));
+        mul_t<1, 2>(A, xa, ps, t0w, 16 * j, 128, lane);
+      }
+    const float2 eg[2] = {vec2(vec + kVecEg + t0w, 0, lane), vec2(vec + kVecEg + t0w, 1, lane)};
+    float2 be[2];
+    {
+      float B[2][4];
+      uint32_t fa[1][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 tl = vec2(vec + kVecTail + t0w, i, lane), tau = vec2(vec + kVecTau + t0w, i, lane);
+        be[i] = vec2(vec + kVecBeta + t0w, i, lane);
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          F[i][r] = ka * fmaf(tl.x, F[i][r], co * A[i][r]);
+          F[i][r + 1] = ka * fmaf(tl.y, F[i][r + 1], co * A[i][r + 1]);
+          B[i][r] = F[i][r] * (be[i].x * tau.x);
+          B[i][r + 1] = F[i][r + 1] * (be[i].y * tau.y);
+        }
+      }
+      to_a<1>(B[0], B[1], fa);
+      stsm4(a_addr(own + L::kR, 0, t0w, 128, lane), fa[0]);
+    }
+    strip_sync(strip);
+    {
+      float C[2][4] = {};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j >= w) {
+          uint32_t fa[1][4];
+          ldsm4(fa[0], a_addr(own + L::kR, 0, 16 * j, 128, lane));
+          mul_t<1, 2>(C, fa, ys, t0w, 16 * j, 128, lane);
+        }
+      float W[2][4], Z[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float c0 = -eg[i].x * ka, c1 = -eg[i].y * ka;
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          F[i][r] -= C[i][r];
+          F[i][r + 1] -= C[i][r + 1];
+          W[i][r] = F[i][r] * (be[i].x * c0);
+          W[i][r + 1] = F[i][r + 1] * (be[i].y * c1);
+          Z[i][r] = X[i][r] * eg[i].x;
+          Z[i][r + 1] = X[i][r + 1] * eg[i].y;
+        }
+      }
+      uint32_t wa[1][4];
+      to_a<1>(W[0], W[1], wa);
+      stsm4(a_addr(own + L::kW, 0, t0w, 128, lane), wa[0]);
+      to_a<1>(Z[0], Z[1], wa);
+      stsm4(a_addr(own + L::kU, 0, t0w, 128, lane), wa[0]);
+    }
+    uint32_t x[4] = {0, 0, 0, 0};
+    {
+      if (c + 1 < nc) load_x(x, c + 1);
+      const float m = fmaxf(__uint_as_float(top_of(x)) * dn, __uint_as_float(top_of<kTiles>(D)));
+      if (lane == 0) mx[4 * (c & 1) + w] = m;
+    }
+    {
+      uint8_t *to = reinterpret_cast<uint8_t *>(o.D16 + (ht * s.P + p0) * N);
+#pragma unroll
+      for (int i = 0; i < 2 * N; i += 128) {
+        const int at = 16 * (i + (threadIdx.x & 127));
+        *reinterpret_cast<uint4 *>(to + at) = *reinterpret_cast<const uint4 *>(gown + L::kS + at);
+      }
+      if ((threadIdx.x & 127) == 0) o.ub[(ht * s.P + p0) >> 4] = up;
+    }
+    strip_sync(strip);
+    {
+      float Z[kTiles][4] = {};
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) D[i][r] *= last;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t wa[1][4], ya[1][4];
+        ldsm4(wa[0], a_addr(own + L::kW, 0, 16 * j, 128, lane));
+        ldsm4(ya[0], a_addr(own + L::kU, 0, 16 * j, 128, lane));
+        mul_t<1, kTiles>(D, wa, ks, n0, 16 * j, NB, lane);
+        mul_t<1, kTiles>(Z, ya, qs, n0, 16 * j, NB, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) D[i][r] = fmaf(co, Z[i][r], D[i][r]);
+    }
+    const int tok = t0w + (lane >> 1);
+    uint32_t rw[4], vw[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        rw[2 * i + r] = pack(F[i][2 * r], F[i][2 * r + 1]);
+        vw[2 * i + r] = pack_bf16(F[i][2 * r] * (be[i].x * up), F[i][2 * r + 1] * (be[i].y * up));
+      }
+    const int64_t at = (ht * kChunk + tok) * s.P + p0 + 8 * (lane & 1);
+    *reinterpret_cast<uint4 *>(o.X16 + at) = *reinterpret_cast<const uint4 *>(gown + ring + row_at(tok, lane & 1));
+    *reinterpret_cast<uint4 *>(o.F16 + at) = turned(gown + ring, own + ring, rw, t0w, lane);
+    const uint4 vv = turned(gown + ring, own + ring, vw, t0w, lane);
+    if (tok < ck.n) put_out(dv + (ck.b + tok) * tok_stride + h * s.P + p0 + 8 * (lane & 1), ovec, vv);
+    move(rescale(strip_top(mx + 4 * (c & 1)), dn));
+    if (c + 1 < nc) take_x(x, c + 1);
+  }
+  cp_wait<0>();
+  if (live && a.dinit != nullptr) store_state<kTiles>(D, a.dinit + row, up, N, lane);
 }
 
-template <int N, int kTerms, bool kSave>
+bool vec16(const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; }
+
+// Strips of a CTA: several share one copy of the chunk's tiles, fewer spread over more SMs.  At most `most`, and
+// only while that still gives 120 of the 152 SMs a CTA.
+int strips_of(const Shape &s, int most) {
+  const int strips = (s.P + 15) / 16;
+  int n = most;
+  while (n > 1 && (n >= 2 * strips || s.nseq * s.H * ((strips + n - 1) / n) < 120)) n /= 2;
+  return n;
+}
+dim3 chain_grid(const Shape &s, int n) {
+  return dim3(unsigned(((s.P + 15) / 16 + n - 1) / n), unsigned(s.H), unsigned(s.nseq));
+}
+
+template <int N, int kTerms, int kStrips, bool kSave>
 cudaError_t go_fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
-  auto kernel = chain_fwd_kernel<N, kTerms, kSave>;
-  constexpr int smem = Fwd<N, kTerms>::kStages * Fwd<N, kTerms>::kStage + sizeof(Control);
-  static_assert(smem <= 227 * 1024, "shared memory");
+  auto kernel = chain_fwd_kernel<N, kTerms, kStrips, kSave>;
+  constexpr int smem = Layout<N, kTerms>::bytes(kStrips);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(unsigned(s.H), unsigned(s.nseq)), kThreads, smem, st>>>(s, a, t);
+  kernel<<<chain_grid(s, kStrips), 128 * kStrips, smem, st>>>(s, a, t, vec16(a.v, s.vs), vec16(a.o, 8));
   return cudaGetLastError();
 }
-template <int N, int kTerms>
-cudaError_t fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
-  return t.S16 != nullptr ? go_fwd<N, kTerms, true>(s, a, t, st) : go_fwd<N, kTerms, false>(s, a, t, st);
+
+template <int N, int kTerms, bool kSave>
+cudaError_t pick_fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
+  // four strips with two terms would need more shared memory than an SM has
+  const int n = strips_of(s, kTerms == 2 && N == 128 ? 2 : 4);
+  if constexpr (kTerms == 1 || N == 64)
+    if (n == 4) return go_fwd<N, kTerms, 4, kSave>(s, a, t, st);
+  return n >= 2 ? go_fwd<N, kTerms, 2, kSave>(s, a, t, st) : go_fwd<N, kTerms, 1, kSave>(s, a, t, st);
 }
+
+template <int N>
+cudaError_t fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
+  const bool save = t.S16 != nullptr;
+  if (a.fin != nullptr) return save ? pick_fwd<N, 2, true>(s, a, t, st) : pick_fwd<N, 2, false>(s, a, t, st);
+  return save ? pick_fwd<N, 1, true>(s, a, t, st) : pick_fwd<N, 1, false>(s, a, t, st);
+}
+
+template <int N, int kStrips>
+cudaError_t go_bwd(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st) {
+  auto kernel = chain_bwd_kernel<N, kStrips>;
+  constexpr int smem = Layout<N, 1>::bytes(kStrips);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<chain_grid(s, kStrips), 128 * kStrips, smem, st>>>(s, a, t, b, vec16(a.dout, 8), vec16(a.dv, 8));
+  return cudaGetLastError();
+}
+
 template <int N>
 cudaError_t bwd(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st) {
-  auto kernel = chain_bwd_kernel<N>;
-  constexpr int smem = Bwd<N>::kStages * Bwd<N>::kStage + sizeof(Control);
-  static_assert(smem <= 227 * 1024, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kernel<<<dim3(unsigned(s.H), unsigned(s.nseq)), kThreads, smem, st>>>(s, a, t, b);
-  return cudaGetLastError();
+  const int n = strips_of(s, 4);
+  return n == 4 ? go_bwd<N, 4>(s, a, t, b, st) : n == 2 ? go_bwd<N, 2>(s, a, t, b, st) : go_bwd<N, 1>(s, a, t, b, st);
 }
 
 }  // namespace
 
 cudaError_t launch_chain_fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
-  if (s.N == 64) return t.planes == 2 ? fwd<64, 2>(s, a, t, st) : fwd<64, 1>(s, a, t, st);
-  return t.planes == 2 ? fwd<128, 2>(s, a, t, st) : fwd<128, 1>(s, a, t, st);
+  return s.N == 64 ? fwd<64>(s, a, t, st) : fwd<128>(s, a, t, st);
 }
 
 cudaError_t launch_chain_bwd(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st) {

@@ -15,10 +15,9 @@
 // does not pass cancels to the last bit's size.)
 //
 // The heads of a group accumulate dq and dk in registers, in ascending order:
-// no slots, one order.  dq's products share one power of two for the whole
-// group, dk's another: the heads' scales relative to the largest are applied to
-// the left operands (exact, and rarely needed).  M1 and M2 go through fp16 once
-// more.
+// no slots, one order.  Their operands share one power of two for the whole
+// group: the strips' scales relative to the largest are applied to the left
+// operands (exact, and rarely needed).  M1 and M2 go through fp16 once more.
 //
 // CTA (chunk slot, group), 8 warps: warp (w % 4, w / 4) has 16 tokens and half
 // of the columns of each product.  What bounds the kernel is the record, 1.75
@@ -38,17 +37,17 @@ using namespace mma16;
 
 constexpr int kThreads = 256;
 constexpr int kPMax = 128;
-constexpr int kRow = 2 * kPMax;              // bytes of a token's row of e and F in shared memory
+constexpr int kRow = 2 * kPMax;              // bytes of a token's row of a [token][p] tile in shared memory
 constexpr int kRows = kChunk * kRow;
 
 template <int N>
 struct Smem {
   uint8_t k[kChunk * N * 2], q[kChunk * N * 2];
-  uint8_t X[kRows], F[kRows], E[2][kRows];          // [token][p] (X in panels); e of this head and the next
+  uint8_t X[kRows], F[kRows], E[2][kRows];          // [token][p]; e of this head and the next
   uint8_t S[kPMax * N * 2], D[kPMax * N * 2];       // [p][n]
   uint8_t m1[kChunk * 128], m2[kChunk * 128];       // [t][s]
   uint4 kk[2][kThreads], qk[2][kThreads];           // each thread's own part of K K^T and Q K^T, fp16
-  float vec[2][kVec], sc[2][4];                     // of this head and the next; up, ub, 2^x
+  float vec[2][kVec], up[2][8], ub[2][8];           // of this head and the next
   float fe[2][kChunk];                              // [head parity]: F.e of each token
   float state[2][2][kChunk], down[2][2][kChunk];    // [head parity][column half]: q.Y1 + k.Y2, k.Z
   float wrow[2][2][kChunk], wcol[2][4][kChunk];     // row sums of W by column half, column sums by token strip
@@ -72,12 +71,11 @@ __device__ __forceinline__ void scale_a(uint32_t (&a)[4], uint32_t f0, uint32_t 
 // d and (kTwo) e, column tiles from n0, += the left operands a and b times 16 rows [k][n] of `tile`.
 template <int kPairs, bool kTwo>
 __device__ __forceinline__ void step_t(float (&d)[2 * kPairs][4], float (&e)[2 * kPairs][4], const uint32_t (&a)[4],
-                                       const uint32_t (&b)[4], uint32_t tile, int rows, int n0, int k0, int lane) {
-  auto at = [&](int r, int j) { return tile + pan(r, j, rows); };
+                                       const uint32_t (&b)[4], uint32_t tile, int n0, int k0, int bytes, int lane) {
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
     uint32_t r[4];
-    ldsm4t(r, bt_addr(at, n0 + 16 * i, k0, lane));
+    ldsm4t(r, bt_addr(tile, n0 + 16 * i, k0, bytes, lane));
     mma(d[2 * i], a, r[0], r[1]);
     mma(d[2 * i + 1], a, r[2], r[3]);
     if (kTwo) {
@@ -89,6 +87,7 @@ __device__ __forceinline__ void step_t(float (&d)[2 * kPairs][4], float (&e)[2 *
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a, Tiles t, BwdTiles o, int out4) {
+  constexpr int NB = 2 * N;          // bytes of a row of k, q, S, D
   constexpr int kPairs = N / 32;     // pairs of column tiles of a warp (half of the columns)
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<N> &sm = *reinterpret_cast<Smem<N> *>(raw);
@@ -101,26 +100,24 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   const int n = int(e - b);
   const uint32_t ks = smem_at(sm.k), qs = smem_at(sm.q), Xs = smem_at(sm.X), Fs = smem_at(sm.F),
                  Ss = smem_at(sm.S), Ds = smem_at(sm.D), m1s = smem_at(sm.m1), m2s = smem_at(sm.m2);
-  auto kat = [&](int r, int j) { return ks + pan(r, j, kChunk); };
-  auto qat = [&](int r, int j) { return qs + pan(r, j, kChunk); };
-  auto xat = [&](int r, int j) { return Xs + pan(r, j, kChunk); };
-  auto fat = [&](int r, int j) { return Fs + swz(r, j, kRow); };
-  auto m1at = [&](int r, int j) { return m1s + swz(r, j, 128); };
-  auto m2at = [&](int r, int j) { return m2s + swz(r, j, 128); };
 
   auto fetch_rows = [&](int i) {   // the [token][p] tiles and the vectors of head i of the group
-    const int64_t ht = slot * s.H + grp * s.hpg + i, at0 = ht * kChunk * P;
+    const int h = grp * s.hpg + i;
+    const int64_t ht = slot * s.H + h, at0 = ht * kChunk * P;
     const uint32_t Es = smem_at(sm.E[i & 1]);
     const int per = P / 8;   // 16-byte pieces of a row
     for (int x = tid; x < kChunk * per; x += kThreads) {
-      const uint32_t at = swz(x / per, x % per, kRow);
+      const int r = x / per, j = x % per;
+      const uint32_t at = swz(r, j, kRow);
+      cp16(Xs + at, o.X16 + at0 + 8 * x);
       cp16(Fs + at, o.F16 + at0 + 8 * x);
       cp16(Es + at, t.E16 + at0 + 8 * x);
     }
-    const __half *X = o.X16 + ht * kChunk * padded(P);
-    for (int x = tid; x < kChunk * int(padded(P)) / 8; x += kThreads) cp16(Xs + 16 * x, X + 8 * x);
     if (tid < kVec / 4) cp16(smem_at(sm.vec[i & 1]) + 16 * tid, t.vec + ht * kVec + 4 * tid);
-    if (tid < 3) sm.sc[i & 1][tid] = tid == 0 ? t.up[ht] : tid == 1 ? o.ub[ht] : o.side[ht * kSide + 1];
+    if (tid < strips) {
+      sm.up[i & 1][tid] = t.up[ht * strips + tid];
+      sm.ub[i & 1][tid] = o.ub[ht * strips + tid];
+    }
     cp_commit();
   };
   auto fetch_state = [&](uint32_t to, const __half *from, int i) {
@@ -138,21 +135,15 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     cp_commit();
     fetch_rows(0);
   }
-  // the group's common powers of two: of dq's terms (e or S with dO), and of dk's (those, and with F or dS)
-  float refq = 0.f, refk = 0.f;
-  for (int x = lane; x < s.hpg; x += 32) {
-    const int64_t at = slot * s.H + grp * s.hpg + x;
-    refq = fmaxf(refq, t.up[at] * o.side[at * kSide + 1]);
-    refk = fmaxf(refk, t.up[at] * o.ub[at]);
+  // the group's common power of two: the largest of the heads' and strips' up * ub
+  float ref = 0.f;
+  for (int x = lane; x < s.hpg * strips; x += 32) {
+    const int64_t at = (slot * s.H + grp * s.hpg) * strips + x;
+    ref = fmaxf(ref, t.up[at] * o.ub[at]);
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    refq = fmaxf(refq, __shfl_xor_sync(~0u, refq, d));
-    refk = fmaxf(refk, __shfl_xor_sync(~0u, refk, d));
-  }
-  refk = fmaxf(refk, refq);
-  const float iq = pow2_inv(refq), ik = pow2_inv(refk), qtok = refq * ik;
-  const uint32_t qtok2 = twice(qtok);
+  for (int d = 16; d > 0; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(~0u, ref, d));
+  const float iref = pow2_inv(ref);
 
   // dg and dbeta of head i, by one warp, two tokens a lane
   auto finish = [&](int i) {
@@ -187,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     for (int y = 0; y < 2; ++y) {
       const int r = 2 * lane + y;
       if (r < n) {
-        static_cast<__nv_bfloat16 *>(a.dg)[(b + r) * s.H + h] = __float2bfloat16_rn(refk * dg[y]);
-        static_cast<__nv_bfloat16 *>(a.dbeta)[(b + r) * s.H + h] = __float2bfloat16_rn(refk * sm.fe[x][r]);
+        static_cast<__nv_bfloat16 *>(a.dg)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * dg[y]);
+        static_cast<__nv_bfloat16 *>(a.dbeta)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * sm.fe[x][r]);
       }
     }
   };
@@ -201,13 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
 #pragma unroll
     for (int k0 = 0; k0 < N; k0 += 16) {
       uint32_t ak[4], aq[4];
-      ldsm4(ak, a_addr(kat, 16 * wm, k0, lane));
-      ldsm4(aq, a_addr(qat, 16 * wm, k0, lane));
+      ldsm4(ak, a_addr(ks, 16 * wm, k0, NB, lane));
+      ldsm4(aq, a_addr(qs, 16 * wm, k0, NB, lane));
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (2 * wn + i <= wm) {
           uint32_t bb[4];
-          ldsm4(bb, b_addr(kat, 32 * wn + 16 * i, k0, lane));
+          ldsm4(bb, b_addr(ks, 32 * wn + 16 * i, k0, NB, lane));
           mma(kk[2 * i], ak, bb[0], bb[1]);
           mma(kk[2 * i + 1], ak, bb[2], bb[3]);
           mma(qk[2 * i], aq, bb[0], bb[1]);
@@ -224,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   }
   // this thread's pair of k or q: rows[r], columns n0 + 8 y + c2
   auto pair_of = [&](const uint8_t *tile, int r, int y) {
-    return unpack(*reinterpret_cast<const uint32_t *>(tile + pan(rows[r], (n0 >> 3) + y, kChunk) + 2 * c2));
+    return unpack(*reinterpret_cast<const uint32_t *>(tile + swz(rows[r], (n0 >> 3) + y, NB) + 2 * c2));
   };
   // adds a head's product to the group's and gives its rows' products with k or q
   auto fold = [&](float (&sum)[2 * kPairs][4], const float (&y)[2 * kPairs][4], const uint8_t *tile, float (&dot)[2]) {
@@ -243,30 +234,37 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     const int x = i & 1;
     const float *vec = sm.vec[x];
     const uint32_t Es = smem_at(sm.E[x]);
-    auto eat = [&](int r, int j) { return Es + swz(r, j, kRow); };
     cp_wait<0>();
     __syncthreads();   // this head's rows are here, the head before is done with states and M
     fetch_state(Ds, o.D16, i);
     fetch_state(Ss, t.S16, i);
     if (i > 0 && warp == 0) finish(i - 1);
     const float ka = vec[kVecKa];
-    const float relx = sm.sc[x][0] * sm.sc[x][2] * iq, relf = sm.sc[x][0] * sm.sc[x][1] * ik;
-    const uint32_t relx2 = twice(relx), relf2 = twice(relf);
+    uint32_t rel[kPMax / 16];   // strips' scales relative to the group's
+    bool even = true;
+#pragma unroll
+    for (int j = 0; j < kPMax / 16; ++j) {
+      const float f = j < strips ? sm.up[x][j] * sm.ub[x][j] * iref : 1.f;
+      rel[j] = twice(f);
+      even &= f == 1.f;
+    }
     uint32_t aX[kPMax / 16][4], aF[kPMax / 16][4];
     {
       float n1[4][4] = {}, n2[4][4] = {};
 #pragma unroll
       for (int j = 0; j < kPMax / 16; ++j)
         if (j < strips) {
-          ldsm4(aX[j], a_addr(xat, 16 * wm, 16 * j, lane));
-          ldsm4(aF[j], a_addr(fat, 16 * wm, 16 * j, lane));
-          if (relx != 1.f) scale_a(aX[j], relx2, relx2);
-          if (relf != 1.f) scale_a(aF[j], relf2, relf2);
+          ldsm4(aX[j], a_addr(Xs, 16 * wm, 16 * j, kRow, lane));
+          ldsm4(aF[j], a_addr(Fs, 16 * wm, 16 * j, kRow, lane));
+          if (!even) {
+            scale_a(aX[j], rel[j], rel[j]);
+            scale_a(aF[j], rel[j], rel[j]);
+          }
 #pragma unroll
           for (int y = 0; y < 2; ++y)
             if (2 * wn + y <= wm) {   // blocks up to the diagonal
               uint32_t bb[4];
-              ldsm4(bb, b_addr(eat, 32 * wn + 16 * y, 16 * j, lane));
+              ldsm4(bb, b_addr(Es, 32 * wn + 16 * y, 16 * j, kRow, lane));
               mma(n1[2 * y], aF[j], bb[0], bb[1]);
               mma(n1[2 * y + 1], aF[j], bb[2], bb[3]);
               mma(n2[2 * y], aX[j], bb[0], bb[1]);
@@ -307,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
             *reinterpret_cast<uint32_t *>(sm.m1 + at) = pack(x0, x1);
             *reinterpret_cast<uint32_t *>(sm.m2 + at) = pack(z0, z1);
             const float2 kf = unpack(r ? kkw.y : kkw.x), qf = unpack(r ? qkw.y : qkw.x);
-            const float v0 = c < rows[r] ? fmaf(x0, kf.x, qtok * (z0 * qf.x)) : 0.f;
-            const float v1 = c + 1 < rows[r] ? fmaf(x1, kf.y, qtok * (z1 * qf.y)) : 0.f;
+            const float v0 = c < rows[r] ? fmaf(x0, kf.x, z0 * qf.x) : 0.f;
+            const float v1 = c + 1 < rows[r] ? fmaf(x1, kf.y, z1 * qf.y) : 0.f;
             wrow[r] += v0 + v1;
             wcol[0] += v0;
             wcol[1] += v1;
@@ -336,17 +334,18 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       for (int y = tid; y < P * N / 8; y += kThreads) {
         const uint4 u = *reinterpret_cast<const uint4 *>(sm.S + 16 * y), v = *reinterpret_cast<const uint4 *>(sm.D + 16 * y);
         const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+        const int j = y / (2 * N);   // the strip
         float acc = 0.f;
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const float2 fu = unpack(uu[z]), fv = unpack(vv[z]);
           acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
         }
-        inner += acc;
+        inner = fmaf(acc, sm.up[x][j] * sm.ub[x][j] * iref, inner);
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) inner += __shfl_xor_sync(~0u, inner, d);
-      if (lane == 0) sm.inner[x][warp] = inner * relf;
+      if (lane == 0) sm.inner[x][warp] = inner;
     }
     uint32_t fx[2], ff[2], fu[2];
 #pragma unroll
@@ -363,11 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       for (int j = 0; j < kPMax / 16; ++j)
         if (j < strips) {
           scale_a(aX[j], fx[0], fx[1]);
-          step_t<kPairs, false>(y1, y1, aX[j], aX[j], Ss, P, n0, 16 * j, lane);
+          step_t<kPairs, false>(y1, y1, aX[j], aX[j], Ss, n0, 16 * j, NB, lane);
         }
       fold(dq, y1, sm.q, state);
-      state[0] *= qtok;
-      state[1] *= qtok;
     }
     {
       float y2[2 * kPairs][4] = {};
@@ -375,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       for (int j = 0; j < kPMax / 16; ++j)
         if (j < strips) {
           scale_a(aF[j], ff[0], ff[1]);
-          step_t<kPairs, false>(y2, y2, aF[j], aF[j], Ss, P, n0, 16 * j, lane);
+          step_t<kPairs, false>(y2, y2, aF[j], aF[j], Ss, n0, 16 * j, NB, lane);
         }
       fold(dk, y2, sm.k, state);
     }
@@ -385,10 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       for (int j = 0; j < kPMax / 16; ++j)
         if (j < strips) {
           uint32_t aE[4];
-          ldsm4(aE, a_addr(eat, 16 * wm, 16 * j, lane));
-          if (relf != 1.f) scale_a(aE, relf2, relf2);
+          ldsm4(aE, a_addr(Es, 16 * wm, 16 * j, kRow, lane));
+          if (!even) scale_a(aE, rel[j], rel[j]);
           scale_a(aE, fu[0], fu[1]);
-          step_t<kPairs, false>(z, z, aE, aE, Ds, P, n0, 16 * j, lane);
+          step_t<kPairs, false>(z, z, aE, aE, Ds, n0, 16 * j, NB, lane);
         }
       fold(dk, z, sm.k, down);
     }
@@ -405,18 +402,17 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
 #pragma unroll 1
     for (int j = 0; j <= wm; ++j) {
       uint32_t a2[4], a1[4];
-      ldsm4(a2, a_addr(m2at, 16 * wm, 16 * j, lane));
-      ldsm4(a1, a_addr(m1at, 16 * wm, 16 * j, lane));
-      step_t<kPairs, true>(dq, dk, a2, a1, ks, kChunk, n0, 16 * j, lane);
+      ldsm4(a2, a_addr(m2s, 16 * wm, 16 * j, 128, lane));
+      ldsm4(a1, a_addr(m1s, 16 * wm, 16 * j, 128, lane));
+      step_t<kPairs, true>(dq, dk, a2, a1, ks, n0, 16 * j, NB, lane);
     }
 #pragma unroll 1
     for (int j = wm; j < 4; ++j) {
       uint32_t a1[4], a2[4];
-      ldsm4t(a1, at_addr(m1at, 16 * wm, 16 * j, lane));
-      ldsm4t(a2, at_addr(m2at, 16 * wm, 16 * j, lane));
-      if (qtok != 1.f) scale_a(a2, qtok2, qtok2);
-      step_t<kPairs, false>(dk, dk, a1, a1, ks, kChunk, n0, 16 * j, lane);
-      step_t<kPairs, false>(dk, dk, a2, a2, qs, kChunk, n0, 16 * j, lane);
+      ldsm4t(a1, at_addr(m1s, 16 * wm, 16 * j, 128, lane));
+      ldsm4t(a2, at_addr(m2s, 16 * wm, 16 * j, 128, lane));
+      step_t<kPairs, false>(dk, dk, a1, a1, ks, n0, 16 * j, NB, lane);
+      step_t<kPairs, false>(dk, dk, a2, a2, qs, n0, 16 * j, NB, lane);
     }
   }
   __syncthreads();
@@ -428,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       const int64_t at = ((b + rows[r]) * s.G + grp) * N + n0 + c2;
 #pragma unroll
       for (int y = 0; y < 2 * kPairs; ++y) {
-        const uint32_t vq = pack_bf16(dq[y][2 * r] * refq, dq[y][2 * r + 1] * refq);
-        const uint32_t vk = pack_bf16(dk[y][2 * r] * refk, dk[y][2 * r + 1] * refk);
+        const uint32_t vq = pack_bf16(dq[y][2 * r] * ref, dq[y][2 * r + 1] * ref);
+        const uint32_t vk = pack_bf16(dk[y][2 * r] * ref, dk[y][2 * r + 1] * ref);
         if (out4) {
           *reinterpret_cast<uint32_t *>(oq + at + 8 * y) = vq;
           *reinterpret_cast<uint32_t *>(ok + at + 8 * y) = vk;

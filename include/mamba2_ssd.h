@@ -481,8 +481,9 @@ const char *mamba2_ssd_delta_path_name(const ssd_delta_dims *dims);
 
 /* Forward.  init_states (nseq, nheads, headdim, dstate) may be NULL (zero);
  * final_states, likewise shaped, may be NULL (not wanted), as may `saved`
- * (no backward will follow), else >= mamba2_ssd_delta_saved_size bytes.
- * States, saved and workspace 16-byte aligned.
+ * (no backward will follow), else >= mamba2_ssd_delta_saved_size bytes; the
+ * workspace is needed only without `saved`.  States, saved and workspace
+ * 16-byte aligned.
  *
  * bf16 with dstate 64 or 128 and headdim a multiple of 16 up to 128 runs the
  * tensor-core kernels ("tiles") in chunks of 64 tokens: matrix operands of 11
@@ -504,15 +505,6 @@ ssd_status mamba2_ssd_delta_bwd(const ssd_delta_dims *dims, const void *q, const
                                 size_t saved_bytes, const void *dout, const float *dfinal, void *dq, void *dk, void *dv,
                                 void *dg, void *dbeta, float *dinit, void *workspace, size_t workspace_bytes,
                                 void *stream);
-
-/* Status of the last forward that used this record (its workspace, where there
- * was no record) or of the last backward that used this workspace: reads one
- * word written by the device (synchronises `stream`).  SSD_ERR_TIMEOUT when a
- * bounded device-side wait ran out, SSD_ERR_UNSUPPORTED when the kernel found
- * its shared memory misaligned and did no work (outputs invalid in both
- * cases), SSD_OK otherwise (always on the general path, which has no
- * device-side waits). */
-ssd_status mamba2_ssd_delta_check(const ssd_delta_dims *dims, const void *record_or_workspace, void *stream);
 
 /* Recurrent form for serving: row b (of batch = nseq) brings seqlen tokens
  * (one, or a few drafted ones) to the state at states[slots[b]] (num_slots,

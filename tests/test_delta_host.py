@@ -57,8 +57,7 @@ def test_delta_rejects_arguments(L):
     assert _delta(L, d, cu=FAKE) == INVALID             # flag not set
     for name in ("init", "fin", "saved", "ws"):
         assert _delta(L, d, **{name: FAKE + 4}) == INVALID
-    assert _delta(L, d, ws=0) == INVALID
-    assert L.mamba2_ssd_delta_check(ctypes.byref(d), None, None) == INVALID
+    assert _delta(L, d, ws=0, saved=0) == INVALID
     need = L.mamba2_ssd_delta_saved_size(ctypes.byref(d))
     assert need > 0 and _delta(L, d, saved_bytes=need - 1) == WORKSPACE
     assert _delta(L, d, saved=0, ws_bytes=L.mamba2_ssd_delta_fwd_workspace_size(ctypes.byref(d)) - 1) == WORKSPACE
