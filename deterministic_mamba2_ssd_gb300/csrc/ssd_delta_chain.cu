@@ -43,18 +43,24 @@ namespace {
 using namespace mma16;
 
 constexpr float kLow = 0.25f, kHigh = 64.f;   // window of a strip's largest value
-constexpr int kStages = 3;    // chunks of tiles in shared memory: one worked on, two on their way
-constexpr int kRing = 4;      // chunks of v (dO) rows: the next chunk's largest value is looked at a chunk ahead
-constexpr int kBlock = kChunk * 32;   // bytes of a strip's rows: 64 tokens x 16
+constexpr int kLoaders = 128;                 // threads that copy
+constexpr int kM = 2;         // warp products a strip is high
+constexpr int kRows = 16 * kM;
+constexpr int kBlock = kChunk * kRows * 2;   // bytes of a strip's part of v: 64 tokens x 32
 
-template <int N, int kTerms>
+template <int N, int kTerms, int kStrips>
 struct Layout {
+  // chunks of tiles in shared memory, one of them worked on; of v (dO) one more is needed, since its largest value is
+  // looked at a chunk ahead
+  static constexpr int kStages = kStrips * kTerms < 4 ? 3 : 2, kRing = kStages + 1;
   static constexpr int kK = 0, kQ = kChunk * N * 2, kY = 2 * kQ, kP = kY + 8192 * kTerms, kVecAt = kP + 8192,
                        kStage = kVecAt + (kVecChain * 4 + 127) / 128 * 128;
   // a strip's own space: ring of v or dO, then the left operands
-  static constexpr int kS = kRing * kBlock, kR = kS + kTerms * 32 * N, kU = kR + kTerms * 2048, kW = kU + 2048,
-                       kMax = kW + kTerms * 2048, kStrip = kMax + 128;
-  __host__ __device__ static constexpr int bytes(int strips) { return kStages * kStage + strips * kStrip; }
+  static constexpr int kRow = kRows * 128, kPlane = kRows * 2 * N;   // bytes of 64 tokens' and of the state's columns
+  static constexpr int kS = kRing * kBlock, kR = kS + kTerms * kPlane, kU = kR + kTerms * kRow, kW = kU + kRow,
+                       kMax = kW + kTerms * kRow, kStrip = kMax + 128;
+  static constexpr int kBytes = kStages * kStage + kStrips * kStrip;
+  static_assert(kBytes <= 232448, "more shared memory than a CTA can have");
 };
 
 struct Chunk {
@@ -62,11 +68,12 @@ struct Chunk {
   int n;             // tokens
 };
 
-// Byte offset of 16-byte half `j` of token t in a strip's 64 x 16 block.
-__device__ __forceinline__ uint32_t row_at(int t, int j) { return t * 32 + ((j ^ ((t >> 2) & 1)) << 4); }
-// This lane's row of a transposing load or store of 16 tokens (4 matrices) of a block: accumulator layout, tokens as columns.
-__device__ __forceinline__ uint32_t block_addr(uint32_t block, int t0, int lane) {
-  return block + row_at(t0 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+// Byte offset of 16-byte piece j (of four) of token t in a strip's 64 x 32 block.
+__device__ __forceinline__ uint32_t row_at(int t, int j) { return t * 64 + ((j ^ ((t >> 1) & 3)) << 4); }
+// This lane's row of a transposing load or store of 16 tokens x 16 rows (4 matrices) of a block: accumulator layout,
+// tokens as columns.
+__device__ __forceinline__ uint32_t block_addr(uint32_t block, int t0, int m, int lane) {
+  return block + row_at(t0 + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1));
 }
 
 __device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
@@ -75,6 +82,15 @@ __device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
                : "memory");
 }
 __device__ __forceinline__ void strip_sync(int strip) { asm volatile("bar.sync %0, 128;" ::"r"(strip + 1) : "memory"); }
+
+// Where a lane's row of a four-matrix load or store begins, for 16 x 16 block 0 of its tile; `block` gives block j
+// along the rows (tiles are aligned to 128 bytes, so the swizzle is an exclusive or of the address itself).
+__device__ __forceinline__ uint32_t lane_row(int lane, int hi_row, int hi_col, int bytes) {   // bits of lane: +8 rows, +8 columns
+  return ((lane & 7) + (((lane >> hi_row) & 1) << 3)) * bytes + (((((lane >> hi_col) & 1)) ^ (lane & 7)) << 4);
+}
+__device__ __forceinline__ uint32_t left_row(int lane, int bytes) { return lane_row(lane, 3, 4, bytes); }
+__device__ __forceinline__ uint32_t right_row(int lane, int bytes) { return lane_row(lane, 4, 3, bytes); }   // tile [n][k]
+__device__ __forceinline__ uint32_t block(uint32_t row, int j) { return (row ^ ((j & 3) << 5)) + ((j >> 2) << 7); }
 
 // 16 x 16 values (two accumulator tiles) rounded, as the four matrices of a store.
 template <int kTerms>
@@ -91,43 +107,80 @@ __device__ __forceinline__ void to_a(const float (&x)[4], const float (&y)[4], u
   }
 }
 
-// The chunk's tiles, copied by all threads of the CTA.
-template <int N, int kTerms, int kThreads>
-__device__ __forceinline__ void fetch_tiles(const Shape &s, const Tiles &t, int64_t slot, int h, uint32_t stage) {
-  using L = Layout<N, kTerms>;
-  const int tid = threadIdx.x;
+// The chunk's tiles, copied by kThreads threads of which this is `tid`.
+template <int N, int kTerms, int kStrips, int kThreads>
+__device__ __forceinline__ void fetch_tiles(const Shape &s, const Tiles &t, int64_t slot, int h, uint32_t stage, int tid) {
+  using L = Layout<N, kTerms, kStrips>;
   const int64_t kt = (slot * s.G + h / s.hpg) * kChunk * N, ht = slot * s.H + h;
   const uint8_t *K = reinterpret_cast<const uint8_t *>(t.K16 + kt) + 16 * tid;
   const uint8_t *Q = reinterpret_cast<const uint8_t *>(t.Q16 + kt) + 16 * tid;
   const uint8_t *Y = reinterpret_cast<const uint8_t *>(t.Y16 + ht * 2 * kTri) + 16 * tid;
   const uint8_t *P = reinterpret_cast<const uint8_t *>(t.P16 + ht * kTri) + 16 * tid;
   stage += 16 * tid;
-#pragma unroll
+#pragma unroll 8
   for (int i = 0; i < kChunk * N / 8; i += kThreads) {
     cp16(stage + L::kK + 16 * i, K + 16 * i);
     cp16(stage + L::kQ + 16 * i, Q + 16 * i);
   }
-#pragma unroll
+#pragma unroll 8
   for (int i = 0; i < 512 * kTerms; i += kThreads) cp16(stage + L::kY + 16 * i, Y + 16 * i);
-#pragma unroll
+#pragma unroll 8
   for (int i = 0; i < 512; i += kThreads) cp16(stage + L::kP + 16 * i, P + 16 * i);
-  if (tid < kVecChain / 4) cp16(stage + L::kVecAt, reinterpret_cast<const uint8_t *>(t.vec + ht * kVec) + 16 * tid);
+  for (int i = tid; i < kVecChain / 4; i += kThreads)
+    cp16(stage + L::kVecAt + 16 * (i - tid), reinterpret_cast<const uint8_t *>(t.vec + ht * kVec) + 16 * i);
 }
 
-// The strip's 16 columns of the chunk's v or dO, one 16-byte piece a thread; tokens past the end are zero.
-__device__ __forceinline__ void fetch_rows(const Chunk &c, const __nv_bfloat16 *x, int64_t stride, int col, bool vec,
-                                           uint32_t block, uint8_t *gblock) {
-  const int i = threadIdx.x & 127, r = i >> 1, j = i & 1;
-  const uint32_t at = row_at(r, j);
-  const __nv_bfloat16 *src = x + (c.b + r) * stride + col + 8 * j;
-  if (vec) {
-    const int n = r < c.n ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(block + at), "l"(n ? src : x), "r"(n) : "memory");
-  } else {
-    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(gblock + at);
+// The strips' columns of the chunk's v or dO; tokens past the end and columns past the head are zero.
+template <int kStrips, int kThreads>
+__device__ __forceinline__ void fetch_rows(const Chunk &c, const __nv_bfloat16 *x, int64_t stride, int p0, int P, bool vec,
+                                           uint32_t at, uint8_t *gat, int step, int tid) {
+#pragma unroll 2
+  for (int i = tid; i < kStrips * kChunk * 4; i += kThreads) {
+    const int strip = i >> 8, r = (i >> 2) & 63, j = i & 3, col = p0 + strip * kRows + 8 * j;
+    const uint32_t to = strip * step + row_at(r, j);
+    const bool on = r < c.n && col < P;
+    const __nv_bfloat16 *src = x + (c.b + r) * stride + col;
+    if (vec) {
+      const int n = on ? 16 : 0;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + to), "l"(n ? src : x), "r"(n) : "memory");
+    } else {
+      __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(gat + to);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dst[e] = r < c.n ? src[e] : __float2bfloat16_rn(0.f);
+      for (int e = 0; e < 8; ++e) dst[e] = on ? src[e] : __float2bfloat16_rn(0.f);
+    }
   }
+}
+
+// What the copying warps do: the tiles of a chunk and the rows of the one after, a stage or two ahead.
+template <int N, int kTerms, int kStrips, int kThreads, class Of>
+__device__ __forceinline__ void copy_in(const Shape &s, const Tiles &t, const __nv_bfloat16 *x, int64_t stride, bool vec,
+                                        int h, int p0, int64_t nc, Of of, uint8_t *smem, int tid) {
+  using L = Layout<N, kTerms, kStrips>;
+  constexpr int kOwn = L::kStages * L::kStage;
+  const uint32_t base = smem_at(smem);
+  auto rows = [&](int64_t c) {
+    if (c < nc) {
+      const int at = kOwn + int(c % L::kRing) * kBlock;
+      fetch_rows<kStrips, kThreads>(of(c), x + h * s.P, stride, p0, s.P, vec, base + at, smem + at, L::kStrip, tid);
+    }
+  };
+  auto fetch = [&](int64_t c) {
+    if (c < nc) fetch_tiles<N, kTerms, kStrips, kThreads>(s, t, of(c).slot, h, base + int(c % L::kStages) * L::kStage, tid);
+    rows(c + 1);
+    cp_commit();
+  };
+  if (nc == 0) return;
+  rows(0);
+  cp_commit();
+  for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
+  cp_wait<L::kStages - 1>();
+  __syncthreads();
+  for (int64_t c = 0; c < nc; ++c) {
+    cp_wait<L::kStages - 2>();
+    __syncthreads();   // tiles of c, rows of c + 1 are here; everyone is done with chunk c - 1
+    fetch(c + L::kStages - 1);
+  }
+  cp_wait<0>();
 }
 
 __device__ __forceinline__ void put_out(__nv_bfloat16 *p, bool vec, uint4 v) {
@@ -143,27 +196,41 @@ __device__ __forceinline__ void put_out(__nv_bfloat16 *p, bool vec, uint4 v) {
   }
 }
 
-// This warp's 16 tokens x 16 rows through its part of `block` to [token][row]: the lane's token and half, and their 8 values.
-__device__ __forceinline__ uint4 turned(uint8_t *gblock, uint32_t block, const uint32_t (&w)[4], int t0, int lane) {
+// This warp's 16 tokens x 32 rows through its part of a block to [token][row]: pieces lane and lane + 32 of 16 bytes.
+__device__ __forceinline__ void turned(uint4 (&v)[2], uint8_t *gblock, uint32_t blk, const uint32_t (&w)[kM][4], int t0,
+                                       int lane) {
   __syncwarp();
-  stsm4t(block_addr(block, t0, lane), w);
+#pragma unroll
+  for (int m = 0; m < kM; ++m) stsm4t(block_addr(blk, t0, m, lane), w[m]);
   __syncwarp();
-  return *reinterpret_cast<const uint4 *>(gblock + row_at(t0 + (lane >> 1), lane & 1));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    v[i] = *reinterpret_cast<const uint4 *>(gblock + row_at(t0 + 8 * i + (lane >> 2), lane & 3));
 }
 
-// Largest magnitude of a warp's bf16 pairs, as the bits of a float.
-__device__ __forceinline__ uint32_t top_of(const uint32_t (&w)[4]) {
+// Largest magnitude of a warp's packed fp16 (NaN counts for more than any number).
+__device__ __forceinline__ float warp_top(uint32_t m) {
+  const uint32_t u = __reduce_max_sync(~0u, max(m & 0x7fffu, (m >> 16) & 0x7fffu));
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+}
+// The larger of each half's magnitude.
+__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7fff7fffu); }
+// Largest magnitude of a warp's bf16 pairs.
+__device__ __forceinline__ float rows_top(const uint32_t (&w)[kM][4]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fff0000u, (w[i] << 16) & 0x7fff0000u));
-  return __reduce_max_sync(~0u, m);
+  for (int i = 0; i < 4 * kM; ++i) m = top2(m, w[i / 4][i % 4]);
+  return __uint_as_float(__reduce_max_sync(~0u, max(m & 0x7fffu, m >> 16)) << 16);
 }
 template <int kTiles>
-__device__ __forceinline__ uint32_t top_of(const float (&S)[kTiles][4]) {
-  float m = 0.f;
+__device__ __forceinline__ float state_top(const float (&S)[kM][kTiles][4]) {
+  float x = 0.f;
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) m = fmaxf(m, fmaxf(fmaxf(fabsf(S[i][0]), fabsf(S[i][1])), fmaxf(fabsf(S[i][2]), fabsf(S[i][3]))));
-  return __reduce_max_sync(~0u, __float_as_uint(m));
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+      x = fmaxf(x, fmaxf(fmaxf(fabsf(S[m][i][0]), fabsf(S[m][i][1])), fmaxf(fabsf(S[m][i][2]), fabsf(S[m][i][3]))));
+  return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(x)));
 }
 
 // Factor that brings a strip's largest value `need` back into the window (1 while it is inside, zero or not finite).
@@ -181,531 +248,630 @@ __device__ __forceinline__ float strip_top(const float *mx) {
   return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
 }
 
+// A strip's running scale: values are held times `dn` = 1 / `up`.
 template <int kTiles>
-__device__ __forceinline__ void load_state(float (&S)[kTiles][4], const float *p, bool on, int N, int lane) {
+struct Scaled {
+  float up = 1.f, dn = 1.f;
+  __device__ __forceinline__ void move(float (&S)[kM][kTiles][4], float f) {
+    if (f == 1.f) return;
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i)
+    for (int m = 0; m < kM; ++m)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float2 v = on ? *reinterpret_cast<const float2 *>(p + int64_t((lane >> 2) + 8 * r) * N + 8 * i + 2 * (lane & 3))
-                          : make_float2(0.f, 0.f);
-      S[i][2 * r] = v.x;
-      S[i][2 * r + 1] = v.y;
-    }
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[m][i][r] *= f;
+    dn *= f;
+    up *= pow2_inv(f);
+  }
+};
+
+// rows: how many of the strip's 32 rows the head has
+template <int kTiles>
+__device__ __forceinline__ void load_state(float (&S)[kM][kTiles][4], const float *p, int rows, int N, int lane) {
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 v = 16 * m < rows ? *reinterpret_cast<const float2 *>(
+                                             p + int64_t(16 * m + (lane >> 2) + 8 * r) * N + 8 * i + 2 * (lane & 3))
+                                       : make_float2(0.f, 0.f);
+        S[m][i][2 * r] = v.x;
+        S[m][i][2 * r + 1] = v.y;
+      }
 }
 template <int kTiles>
-__device__ __forceinline__ void store_state(const float (&S)[kTiles][4], float *p, float up, int N, int lane) {
+__device__ __forceinline__ void store_state(const float (&S)[kM][kTiles][4], float *p, float up, int rows, int N, int lane) {
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i)
+  for (int m = 0; m < kM; ++m)
+    if (16 * m < rows)
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      *reinterpret_cast<float2 *>(p + int64_t((lane >> 2) + 8 * r) * N + 8 * i + 2 * (lane & 3)) =
-          make_float2(S[i][2 * r] * up, S[i][2 * r + 1] * up);
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<float2 *>(p + int64_t(16 * m + (lane >> 2) + 8 * r) * N + 8 * i + 2 * (lane & 3)) =
+              make_float2(S[m][i][2 * r] * up, S[m][i][2 * r + 1] * up);
 }
 
 __device__ __forceinline__ float2 vec2(const float *v, int i, int lane) {
   return *reinterpret_cast<const float2 *>(v + 8 * i + 2 * (lane & 3));
 }
 
-// d (two token tiles) += left operand (16 x 16 at column k0 of `a`, rows of `ab` bytes) times 16 rows [n][k] of `tile`.
+// Two neighbouring accumulator tiles of each of the strip's products += its left operands a times one right operand.
 template <int kTerms>
-__device__ __forceinline__ void mul_n(float (&d)[2][4], const uint32_t (&a)[kTerms][4], uint32_t tile, int n0, int k0,
-                                      int bytes, int lane) {
-  uint32_t b[4];
-  ldsm4(b, b_addr(tile, n0, k0, bytes, lane));
+__device__ __forceinline__ void mul(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[kTerms][4], const uint32_t (&b)[4]) {
 #pragma unroll
   for (int t = 0; t < kTerms; ++t) {
-    mma(d[0], a[t], b[0], b[1]);
-    mma(d[1], a[t], b[2], b[3]);
+    mma(d0, a[t], b[0], b[1]);
+    mma(d1, a[t], b[2], b[3]);
   }
 }
-// The same, kTiles column tiles from n0, with `tile` as rows [k][n].
-template <int kTerms, int kTiles>
-__device__ __forceinline__ void mul_t(float (&d)[kTiles][4], const uint32_t (&a)[kTerms][4], uint32_t tile, int n0, int k0,
-                                      int bytes, int lane) {
+
+// The state's fp16 terms to the strip's space, by each warp for its columns (`at`: its lane's row of the left operand,
+// j0: the first 16 of its columns), and with kRecord the first term to the record.  Returns the largest magnitudes.
+template <int N, int kTerms, bool kRecord, int kTiles>
+__device__ __forceinline__ uint32_t put_state(const float (&S)[kM][kTiles][4], uint32_t at, int plane, int j0, __half *record,
+                                              int rows, int lane) {
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kTiles / 2; ++i) {
-    uint32_t b[4];
-    ldsm4t(b, bt_addr(tile, n0 + 16 * i, k0, bytes, lane));
+  for (int m = 0; m < kM; ++m)
 #pragma unroll
-    for (int t = 0; t < kTerms; ++t) {
-      mma(d[2 * i], a[t], b[0], b[1]);
-      mma(d[2 * i + 1], a[t], b[2], b[3]);
+    for (int i = 0; i < kTiles / 2; ++i) {
+      uint32_t a[kTerms][4];
+      to_a<kTerms>(S[m][2 * i], S[m][2 * i + 1], a);
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t) stsm4(block(at, j0 + i) + m * 32 * N + t * plane, a[t]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) top = top2(top, a[0][r]);
+      if (kRecord && 16 * m < rows) {
+        uint8_t *to = reinterpret_cast<uint8_t *>(record) + 4 * (lane & 3);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<uint32_t *>(to + swz(16 * m + (lane >> 2) + 8 * (r & 1), 2 * (j0 + i) + (r >> 1), 2 * N)) = a[0][r];
+      }
     }
-  }
+  return top;
 }
 
-// The state's fp16 terms to the strip's space; called by each warp for its columns.
-template <int kTerms, int kTiles>
-__device__ __forceinline__ void put_state(const float (&S)[kTiles][4], uint32_t at, int plane, int n0, int bytes, int lane) {
-#pragma unroll
-  for (int i = 0; i < kTiles / 2; ++i) {
-    uint32_t a[kTerms][4];
-    to_a<kTerms>(S[2 * i], S[2 * i + 1], a);
-#pragma unroll
-    for (int t = 0; t < kTerms; ++t) stsm4(a_addr(at + t * plane, 0, n0 + 16 * i, bytes, lane), a[t]);
-  }
-}
-
-// CTA (kStrips strips of 16 rows, head, sequence), four warps a strip.
+// CTA (kStrips strips of 32 rows, head, sequence): four warps a strip, and the warps that copy.
 template <int N, int kTerms, int kStrips, bool kSave>
-__global__ void __launch_bounds__(128 * kStrips) chain_fwd_kernel(Shape s, Args a, Tiles t, int vvec, int ovec) {
-  using L = Layout<N, kTerms>;
-  constexpr int kTiles = N / 32, NB = 2 * N, kPlane = 32 * N;
-  extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(Shape s, Args a, Tiles t, int vvec,
+                                                                                          int ovec) {
+  using L = Layout<N, kTerms, kStrips>;
+  constexpr int kTiles = N / 32, NB = 2 * N;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
-  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * 16, n0 = w * (N / 4), t0w = 16 * w;
-  const bool live = p0 < s.P;
+  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * kRows, n0 = w * (N / 4), t0w = 16 * w;
   const int64_t seq = blockIdx.z;
   int64_t t0, te;
   seq_range(s, a.cu, seq, t0, te);
   const int64_t slot0 = first_slot(s, a.cu, seq, t0), nc = (te - t0 + kChunk - 1) / kChunk;
-  const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v);
-  __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
-  const uint32_t base = smem_at(smem), own = base + kStages * L::kStage + strip * L::kStrip;
-  uint8_t *gown = smem + kStages * L::kStage + strip * L::kStrip;
-  float *mx = reinterpret_cast<float *>(gown + L::kMax);
   auto chunk = [&](int64_t c) {
-    return Chunk{min(slot0 + c, s.slots - 1), t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
+    return Chunk{slot0 + c, t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
   };
-  auto fetch_v = [&](int64_t c) {
-    if (c < nc && live) {
-      const int at = int(c % kRing) * kBlock;
-      fetch_rows(chunk(c), v, s.vs, h * s.P + p0, vvec, own + at, gown + at);
-    }
-  };
-  auto fetch = [&](int64_t c) {   // the tiles of chunk c and the rows of the one after
-    if (c < nc) fetch_tiles<N, kTerms, 128 * kStrips>(s, t, chunk(c).slot, h, base + int(c % kStages) * L::kStage);
-    fetch_v(c + 1);
-    cp_commit();
-  };
-  float S[kTiles][4], up = 1.f, dn = 1.f;
+  if (strip == kStrips) {
+    copy_in<N, kTerms, kStrips, kLoaders>(s, t, static_cast<const __nv_bfloat16 *>(a.v), s.vs, vvec, h,
+                                                    int(blockIdx.x) * kStrips * kRows, nc, chunk, smem, threadIdx.x & 127);
+    return;
+  }
+  const int rows = s.P - p0;
+  const bool live = rows > 0;
+  __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
+  const uint32_t base = smem_at(smem), own = base + L::kStages * L::kStage + strip * L::kStrip;
+  uint8_t *gown = smem + L::kStages * L::kStage + strip * L::kStrip;
+  float *mx = reinterpret_cast<float *>(gown + L::kMax);
+  const uint32_t Srow = own + L::kS + left_row(lane, NB), Rrow = own + L::kR + left_row(lane, 128),
+                 Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128);
+  float S[kM][kTiles][4];
+  Scaled<kTiles> sc;
   const int64_t row = ((seq * s.H + h) * s.P + p0) * N + n0;
-  load_state<kTiles>(S, a.init + row, live && a.init != nullptr, N, lane);
-  fetch_v(0);
-  cp_commit();
-  fetch(0);
-  fetch(1);
+  load_state<kTiles>(S, a.init + row, a.init != nullptr ? rows : 0, N, lane);
   // v of chunk c, this warp's tokens, as packed pairs
-  auto load_v = [&](uint32_t (&x)[4], int64_t c) { ldsm4t(x, block_addr(own + int(c % kRing) * kBlock, t0w, lane)); };
-  auto move = [&](float f) {
-    if (f != 1.f) {
+  auto load_v = [&](uint32_t (&x)[kM][4], int64_t c) {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) S[i][r] *= f;
-      dn *= f;
-      up *= pow2_inv(f);
-    }
+    for (int m = 0; m < kM; ++m) ldsm4t(x[m], block_addr(own + int(c % L::kRing) * kBlock, t0w, m, lane));
   };
   if (nc > 0) {
-    cp_wait<2>();
     __syncthreads();
     if (live) {
-      uint32_t x[4];
+      uint32_t x[kM][4];
       load_v(x, 0);
-      const float m = fmaxf(__uint_as_float(top_of(x)), __uint_as_float(top_of<kTiles>(S)));
+      const float m = fmaxf(rows_top(x), state_top<kTiles>(S));
       if (lane == 0) mx[4 + w] = m;
       strip_sync(strip);
-      move(rescale(strip_top(mx + 4), 1.f));
+      sc.move(S, rescale(strip_top(mx + 4), 1.f));
     }
   }
   for (int64_t c = 0; c < nc; ++c) {
-    if (live) put_state<kTerms, kTiles>(S, own + L::kS, kPlane, n0, NB, lane);
-    cp_wait<1>();
-    __syncthreads();   // tiles of c, rows of c + 1, S of every warp; everyone is done with chunk c - 1
-    fetch(c + 2);
-    if (!live) continue;
     const Chunk ck = chunk(c);
     const int64_t ht = ck.slot * s.H + h;
-    const int stage = int(c % kStages) * L::kStage, ring = int(c % kRing) * kBlock;
-    const uint32_t ks = base + stage + L::kK, qs = base + stage + L::kQ, ys = base + stage + L::kY, ps = base + stage + L::kP;
+    uint32_t top = 0;
+    if (live) {
+      top = put_state<N, kTerms, kSave>(S, Srow, L::kPlane, w * (N / 64), kSave ? t.S16 + (ht * s.P + p0) * N : nullptr, rows,
+                                        lane);
+      if (kSave && (threadIdx.x & 127) < kM && 16 * (threadIdx.x & 127) < rows)
+        t.up[((ht * s.P + p0) >> 4) + (threadIdx.x & 127)] = sc.up;
+    }
+    __syncthreads();   // tiles of c, rows of c + 1, S of every warp
+    if (!live) continue;
+    const int stage = int(c % L::kStages) * L::kStage, ring = int(c % L::kRing) * kBlock;
+    const uint32_t tiles = base + stage;
     const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
     const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1];
     const float2 eg[2] = {vec2(vec + kVecEg + t0w, 0, lane), vec2(vec + kVecEg + t0w, 1, lane)};
-    uint32_t vw[4];
-    load_v(vw, c);
-    float R[2][4] = {}, O[2][4] = {};
+    float R[kM][2][4] = {}, O[kM][2][4] = {};
+    {
+      const uint32_t krow = tiles + L::kK + t0w * NB + right_row(lane, NB);
 #pragma unroll
-    for (int j = 0; j < N / 16; ++j) {
-      uint32_t sa[kTerms][4], one[1][4];
+      for (int j = 0; j < N / 16; ++j) {
+        uint32_t sa[kM][kTerms][4], kb[4], qb[4];
 #pragma unroll
-      for (int i = 0; i < kTerms; ++i) ldsm4(sa[i], a_addr(own + L::kS + i * kPlane, 0, 16 * j, NB, lane));
+        for (int m = 0; m < kM; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) one[0][i] = sa[0][i];
-      mul_n<kTerms>(R, sa, ks, t0w, 16 * j, NB, lane);
-      mul_n<1>(O, one, qs, t0w, 16 * j, NB, lane);
-    }
+          for (int i = 0; i < kTerms; ++i) ldsm4(sa[m][i], block(Srow, j) + m * 16 * NB + i * L::kPlane);
+        ldsm4(kb, block(krow, j));
+        ldsm4(qb, block(krow, j) + (L::kQ - L::kK));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 v0 = unpack_bf16(vw[2 * i]), v1 = unpack_bf16(vw[2 * i + 1]);
-      const float c0 = eg[i].x * ka, c1 = eg[i].y * ka;
-      R[i][0] = fmaf(-c0, R[i][0], v0.x * dn);
-      R[i][1] = fmaf(-c1, R[i][1], v0.y * dn);
-      R[i][2] = fmaf(-c0, R[i][2], v1.x * dn);
-      R[i][3] = fmaf(-c1, R[i][3], v1.y * dn);
+        for (int m = 0; m < kM; ++m) {
+          mul<kTerms>(R[m][0], R[m][1], sa[m], kb);
+          mma(O[m][0], sa[m][0], qb[0], qb[1]);
+          mma(O[m][1], sa[m][0], qb[2], qb[3]);
+        }
+      }
     }
     float2 be[2];
     {
-      float B[2][4];
-      uint32_t ra[kTerms][4];
+      uint32_t vw[kM][4];
+      load_v(vw, c);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        be[i] = vec2(vec + kVecBeta + t0w, i, lane);
+      for (int i = 0; i < 2; ++i) be[i] = vec2(vec + kVecBeta + t0w, i, lane);
 #pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          B[i][r] = R[i][r] * be[i].x;
-          B[i][r + 1] = R[i][r + 1] * be[i].y;
-        }
-      }
-      to_a<kTerms>(B[0], B[1], ra);
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) stsm4(a_addr(own + L::kR + 2048 * i, 0, t0w, 128, lane), ra[i]);
-    }
-    strip_sync(strip);
-    float E[2][4] = {};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= w) {
+      for (int m = 0; m < kM; ++m) {
+        float B[2][4];
         uint32_t ra[kTerms][4];
 #pragma unroll
-        for (int i = 0; i < kTerms; ++i) ldsm4(ra[i], a_addr(own + L::kR + 2048 * i, 0, 16 * j, 128, lane));
-        mul_n<kTerms>(E, ra, ys, t0w, 16 * j, 128, lane);
-        if constexpr (kTerms == 2) {
-          uint32_t one[1][4] = {{ra[0][0], ra[0][1], ra[0][2], ra[0][3]}};
-          mul_n<1>(E, one, ys + 8192, t0w, 16 * j, 128, lane);
+        for (int i = 0; i < 2; ++i) {
+          const float c0 = eg[i].x * ka, c1 = eg[i].y * ka;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 v = unpack_bf16(vw[m][2 * i + r]);
+            R[m][i][2 * r] = fmaf(-c0, R[m][i][2 * r], v.x * sc.dn);
+            R[m][i][2 * r + 1] = fmaf(-c1, R[m][i][2 * r + 1], v.y * sc.dn);
+            B[i][2 * r] = R[m][i][2 * r] * be[i].x;
+            B[i][2 * r + 1] = R[m][i][2 * r + 1] * be[i].y;
+          }
         }
-      }
-    float W[2][4];
-    uint32_t ew[4];
+        to_a<kTerms>(B[0], B[1], ra);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 tau = vec2(vec + kVecTau + t0w, i, lane), tl = vec2(vec + kVecTail + t0w, i, lane);
-      const float c0 = be[i].x * ka, c1 = be[i].y * ka;
-#pragma unroll
-      for (int r = 0; r < 4; r += 2) {
-        const float e0 = fmaf(-tau.x, E[i][r], R[i][r]), e1 = fmaf(-tau.y, E[i][r + 1], R[i][r + 1]);
-        if (kSave) ew[2 * i + r / 2] = pack(e0, e1);
-        E[i][r] = e0 * c0;
-        E[i][r + 1] = e1 * c1;
-        W[i][r] = E[i][r] * tl.x;
-        W[i][r + 1] = E[i][r + 1] * tl.y;
+        for (int i = 0; i < kTerms; ++i) stsm4(block(Rrow, w) + m * 2048 + i * L::kRow, ra[i]);
       }
     }
+    strip_sync(strip);
+    uint32_t ew[kM][4];
     {
-      uint32_t ua[1][4], wa[kTerms][4];
-      to_a<kTerms>(W[0], W[1], wa);
+      float E[kM][2][4] = {};
+      const uint32_t yrow = tiles + L::kY + t0w * 128 + right_row(lane, 128);
 #pragma unroll
-      for (int i = 0; i < kTerms; ++i) stsm4(a_addr(own + L::kW + 2048 * i, 0, t0w, 128, lane), wa[i]);
-      to_a<1>(E[0], E[1], ua);
-      stsm4(a_addr(own + L::kU, 0, t0w, 128, lane), ua[0]);
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) {
+          uint32_t ra[kM][kTerms][4], yb[kTerms][4];
+#pragma unroll
+          for (int i = 0; i < kTerms; ++i) {
+#pragma unroll
+            for (int m = 0; m < kM; ++m) ldsm4(ra[m][i], block(Rrow, j) + m * 2048 + i * L::kRow);
+            ldsm4(yb[i], block(yrow, j) + i * 8192);
+          }
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            mul<kTerms>(E[m][0], E[m][1], ra[m], yb[0]);
+            if (kTerms == 2) {
+              mma(E[m][0], ra[m][0], yb[kTerms - 1][0], yb[kTerms - 1][1]);
+              mma(E[m][1], ra[m][0], yb[kTerms - 1][2], yb[kTerms - 1][3]);
+            }
+          }
+        }
+      float2 tau[2], tl[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        tau[i] = vec2(vec + kVecTau + t0w, i, lane);
+        tl[i] = vec2(vec + kVecTail + t0w, i, lane);
+      }
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        float W[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const float e0 = fmaf(-tau[i].x, E[m][i][r], R[m][i][r]), e1 = fmaf(-tau[i].y, E[m][i][r + 1], R[m][i][r + 1]);
+            if (kSave) ew[m][2 * i + r / 2] = pack(e0, e1);
+            E[m][i][r] = e0 * (be[i].x * ka);
+            E[m][i][r + 1] = e1 * (be[i].y * ka);
+            W[i][r] = E[m][i][r] * tl[i].x;
+            W[i][r + 1] = E[m][i][r + 1] * tl[i].y;
+          }
+        uint32_t ua[1][4], wa[kTerms][4];
+        to_a<kTerms>(W[0], W[1], wa);
+#pragma unroll
+        for (int i = 0; i < kTerms; ++i) stsm4(block(Wrow, w) + m * 2048 + i * L::kRow, wa[i]);
+        to_a<1>(E[m][0], E[m][1], ua);
+        stsm4(block(Urow, w) + m * 2048, ua[0]);
+      }
     }
     {
       // the next chunk's scale: its rows, and this chunk's state (which one chunk cannot carry out of fp16's range)
-      uint32_t x[4] = {0, 0, 0, 0};
-      if (c + 1 < nc) load_v(x, c + 1);
-      const float m = fmaxf(__uint_as_float(top_of(x)) * dn, __uint_as_float(top_of<kTiles>(S)));
+      float m = warp_top(top);
+      if (m < 0x1p-10f) m = state_top<kTiles>(S);   // too small for fp16 to say
+      if (c + 1 < nc) {
+        uint32_t x[kM][4];
+        load_v(x, c + 1);
+        m = fmaxf(m, rows_top(x) * sc.dn);
+      }
       if (lane == 0) mx[4 * (c & 1) + w] = m;
     }
-    if (kSave) {
-      // the state entering the chunk as it stands in shared memory: 16 rows, contiguous in the record
-      uint8_t *to = reinterpret_cast<uint8_t *>(t.S16 + (ht * s.P + p0) * N);
 #pragma unroll
-      for (int i = 0; i < 2 * N; i += 128) {
-        const int at = 16 * (i + (threadIdx.x & 127));
-        *reinterpret_cast<uint4 *>(to + at) = *reinterpret_cast<const uint4 *>(gown + L::kS + at);
-      }
-      if ((threadIdx.x & 127) == 0) t.up[(ht * s.P + p0) >> 4] = up;
-    }
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[m][i][r] *= last;
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          O[m][i][r] *= eg[i].x;
+          O[m][i][r + 1] *= eg[i].y;
+        }
     strip_sync(strip);
+    {
+      const uint32_t kcol = tiles + L::kK + ((n0 >> 6) << 7) + (lane_row(lane, 3, 4, NB) ^ ((n0 & 63) << 1));
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i)
+      for (int j = 0; j < 4; ++j) {
+        uint32_t wa[kM][kTerms][4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] *= last;
+        for (int m = 0; m < kM; ++m)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t wa[kTerms][4];
+          for (int i = 0; i < kTerms; ++i) ldsm4(wa[m][i], block(Wrow, j) + m * 2048 + i * L::kRow);
 #pragma unroll
-      for (int i = 0; i < kTerms; ++i) ldsm4(wa[i], a_addr(own + L::kW + 2048 * i, 0, 16 * j, 128, lane));
-      mul_t<kTerms, kTiles>(S, wa, ks, n0, 16 * j, NB, lane);
+        for (int i = 0; i < kTiles / 2; ++i) {
+          uint32_t kb[4];
+          ldsm4t(kb, (kcol ^ (i << 5)) + j * 16 * NB);
+#pragma unroll
+          for (int m = 0; m < kM; ++m) mul<kTerms>(S[m][2 * i], S[m][2 * i + 1], wa[m], kb);
+        }
+      }
     }
+    {
+      const uint32_t prow = tiles + L::kP + t0w * 128 + right_row(lane, 128);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) {
+          uint32_t pb[4];
+          ldsm4(pb, block(prow, j));
 #pragma unroll
-      for (int r = 0; r < 4; r += 2) {
-        O[i][r] *= eg[i].x;
-        O[i][r + 1] *= eg[i].y;
-      }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= w) {
-        uint32_t ua[1][4];
-        ldsm4(ua[0], a_addr(own + L::kU, 0, 16 * j, 128, lane));
-        mul_n<1>(O, ua, ps, t0w, 16 * j, 128, lane);
-      }
+          for (int m = 0; m < kM; ++m) {
+            uint32_t ua[1][4];
+            ldsm4(ua[0], block(Urow, j) + m * 2048);
+            mul<1>(O[m][0], O[m][1], ua, pb);
+          }
+        }
+    }
     // outputs and record through this warp's tokens of the v block, which it alone has read
-    const int tok = t0w + (lane >> 1);
-    const float co = a.scale * ka * up;
-    uint32_t ow[4];
+    const float co = a.scale * ka * sc.up;
+    uint32_t ow[kM][4];
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ow[m][i] = pack_bf16(O[m][i >> 1][2 * (i & 1)] * co, O[m][i >> 1][2 * (i & 1) + 1] * co);
+    uint4 out[2];
+    turned(out, gown + ring, own + ring, ow, t0w, lane);
+    const int col = 8 * (lane & 3);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      ow[2 * i] = pack_bf16(O[i][0] * co, O[i][1] * co);
-      ow[2 * i + 1] = pack_bf16(O[i][2] * co, O[i][3] * co);
+      const int tok = t0w + 8 * i + (lane >> 2);
+      if (tok < ck.n && col < rows) put_out(o + ((ck.b + tok) * s.H + h) * s.P + p0 + col, ovec, out[i]);
     }
-    const uint4 ov = turned(gown + ring, own + ring, ow, t0w, lane);
-    if (tok < ck.n) put_out(o + ((ck.b + tok) * s.H + h) * s.P + p0 + 8 * (lane & 1), ovec, ov);
-    if (kSave)
-      *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + tok) * s.P + p0 + 8 * (lane & 1)) =
-          turned(gown + ring, own + ring, ew, t0w, lane);
-    move(rescale(strip_top(mx + 4 * (c & 1)), dn));
+    if (kSave) {
+      turned(out, gown + ring, own + ring, ew, t0w, lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (col < rows)
+          *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + t0w + 8 * i + (lane >> 2)) * s.P + p0 + col) = out[i];
+    }
+    sc.move(S, rescale(strip_top(mx + 4 * (c & 1)), sc.dn));
   }
-  cp_wait<0>();
-  if (live && a.fin != nullptr) store_state<kTiles>(S, a.fin + row, up, N, lane);
+  if (live && a.fin != nullptr) store_state<kTiles>(S, a.fin + row, sc.up, rows, N, lane);
 }
 
 // The reverse recurrence; writes dv, dinit, and for the gradient kernel dS leaving each chunk (D16), F (F16) and dO (X16).
 template <int N, int kStrips>
-__global__ void __launch_bounds__(128 * kStrips) chain_bwd_kernel(Shape s, Args a, Tiles t, BwdTiles o, int gvec, int ovec) {
-  using L = Layout<N, 1>;
+__global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(Shape s, Args a, Tiles t,
+                                                                                          BwdTiles o, int gvec, int ovec) {
+  using L = Layout<N, 1, kStrips>;
   constexpr int kTiles = N / 32, NB = 2 * N;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
-  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * 16, n0 = w * (N / 4), t0w = 16 * w;
-  const bool live = p0 < s.P;
+  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * kRows, n0 = w * (N / 4), t0w = 16 * w;
   const int64_t seq = blockIdx.z, tok_stride = int64_t(s.H) * s.P;
   int64_t t0, te;
   seq_range(s, a.cu, seq, t0, te);
   const int64_t slot0 = first_slot(s, a.cu, seq, t0), nc = (te - t0 + kChunk - 1) / kChunk;
-  const __nv_bfloat16 *go = static_cast<const __nv_bfloat16 *>(a.dout);
-  __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv);
-  const uint32_t base = smem_at(smem), own = base + kStages * L::kStage + strip * L::kStrip;
-  uint8_t *gown = smem + kStages * L::kStage + strip * L::kStrip;
-  float *mx = reinterpret_cast<float *>(gown + L::kMax);
   // step i of the sweep takes chunk nc - 1 - i of the sequence
   auto chunk = [&](int64_t i) {
     const int64_t c = nc - 1 - i;
-    return Chunk{min(slot0 + c, s.slots - 1), t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
+    return Chunk{slot0 + c, t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
   };
-  auto fetch_x = [&](int64_t c) {
-    if (c < nc && live) {
-      const int at = int(c % kRing) * kBlock;
-      fetch_rows(chunk(c), go, tok_stride, h * s.P + p0, gvec, own + at, gown + at);
-    }
-  };
-  auto fetch = [&](int64_t c) {
-    if (c < nc) fetch_tiles<N, 1, 128 * kStrips>(s, t, chunk(c).slot, h, base + int(c % kStages) * L::kStage);
-    fetch_x(c + 1);
-    cp_commit();
-  };
-  float D[kTiles][4], up = 1.f, dn = 1.f;
+  if (strip == kStrips) {
+    copy_in<N, 1, kStrips, kLoaders>(s, t, static_cast<const __nv_bfloat16 *>(a.dout), tok_stride, gvec, h,
+                                               int(blockIdx.x) * kStrips * kRows, nc, chunk, smem, threadIdx.x & 127);
+    return;
+  }
+  const int rows = s.P - p0;
+  const bool live = rows > 0;
+  __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv);
+  const uint32_t base = smem_at(smem), own = base + L::kStages * L::kStage + strip * L::kStrip;
+  uint8_t *gown = smem + L::kStages * L::kStage + strip * L::kStrip;
+  float *mx = reinterpret_cast<float *>(gown + L::kMax);
+  const uint32_t Srow = own + L::kS + left_row(lane, NB), Rrow = own + L::kR + left_row(lane, 128),
+                 Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128);
+  float D[kM][kTiles][4];
+  Scaled<kTiles> sc;
   const int64_t row = ((seq * s.H + h) * s.P + p0) * N + n0;
-  load_state<kTiles>(D, a.dfinal + row, live && a.dfinal != nullptr, N, lane);
-  fetch_x(0);
-  cp_commit();
-  fetch(0);
-  fetch(1);
-  // dO of this warp's tokens in units of the strip's scale; its fp16 takes the place of dO in the ring
-  float X[2][4];
-  auto take_x = [&](const uint32_t (&x)[4], int64_t c) {
+  load_state<kTiles>(D, a.dfinal + row, a.dfinal != nullptr ? rows : 0, N, lane);
+  // dO of this warp's tokens in units of the strip's scale: as fp16 it takes the place of dO in the ring
+  auto take_x = [&](const uint32_t (&x)[kM][4], int64_t c) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 v0 = unpack_bf16(x[2 * i]), v1 = unpack_bf16(x[2 * i + 1]);
-      X[i][0] = v0.x * dn;
-      X[i][1] = v0.y * dn;
-      X[i][2] = v1.x * dn;
-      X[i][3] = v1.y * dn;
+    for (int m = 0; m < kM; ++m) {
+      uint32_t xa[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack_bf16(x[m][i]);
+        xa[i] = pack(v.x * sc.dn, v.y * sc.dn);
+      }
+      stsm4t(block_addr(own + int(c % L::kRing) * kBlock, t0w, m, lane), xa);
     }
-    uint32_t xa[1][4];
-    to_a<1>(X[0], X[1], xa);
-    stsm4t(block_addr(own + int(c % kRing) * kBlock, t0w, lane), xa[0]);
   };
-  auto load_x = [&](uint32_t (&x)[4], int64_t c) { ldsm4t(x, block_addr(own + int(c % kRing) * kBlock, t0w, lane)); };
-  auto move = [&](float f) {
-    if (f != 1.f) {
+  auto load_x = [&](uint32_t (&x)[kM][4], int64_t c) {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) D[i][r] *= f;
-      dn *= f;
-      up *= pow2_inv(f);
-    }
+    for (int m = 0; m < kM; ++m) ldsm4t(x[m], block_addr(own + int(c % L::kRing) * kBlock, t0w, m, lane));
   };
   if (nc > 0) {
-    cp_wait<2>();
     __syncthreads();
     if (live) {
-      uint32_t x[4];
+      uint32_t x[kM][4];
       load_x(x, 0);
-      const float m = fmaxf(__uint_as_float(top_of(x)), __uint_as_float(top_of<kTiles>(D)));
+      const float m = fmaxf(rows_top(x), state_top<kTiles>(D));
       if (lane == 0) mx[4 + w] = m;
       strip_sync(strip);
-      move(rescale(strip_top(mx + 4), 1.f));
+      sc.move(D, rescale(strip_top(mx + 4), 1.f));
       take_x(x, 0);
     }
   }
   for (int64_t c = 0; c < nc; ++c) {
-    if (live) put_state<1, kTiles>(D, own + L::kS, 0, n0, NB, lane);
-    cp_wait<1>();
-    __syncthreads();   // tiles of c, rows of c + 1, dS and dO of every warp; everyone is done with chunk c - 1
-    fetch(c + 2);
-    if (!live) continue;
     const Chunk ck = chunk(c);
     const int64_t ht = ck.slot * s.H + h;
-    const int stage = int(c % kStages) * L::kStage, ring = int(c % kRing) * kBlock;
-    const uint32_t ks = base + stage + L::kK, qs = base + stage + L::kQ, ys = base + stage + L::kY, ps = base + stage + L::kP;
+    uint32_t top = 0;
+    if (live) {
+      top = put_state<N, 1, true>(D, Srow, L::kPlane, w * (N / 64), o.D16 + (ht * s.P + p0) * N, rows, lane);
+      if ((threadIdx.x & 127) < kM && 16 * (threadIdx.x & 127) < rows) o.ub[((ht * s.P + p0) >> 4) + (threadIdx.x & 127)] = sc.up;
+    }
+    __syncthreads();   // tiles of c, rows of c + 1, dS and dO of every warp
+    if (!live) continue;
+    const int stage = int(c % L::kStages) * L::kStage, ring = int(c % L::kRing) * kBlock;
+    const uint32_t tiles = base + stage;
     const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
     const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1], co = a.scale * ka;
-    float F[2][4] = {}, A[2][4] = {};
-#pragma unroll
-    for (int j = 0; j < N / 16; ++j) {
-      uint32_t da[1][4];
-      ldsm4(da[0], a_addr(own + L::kS, 0, 16 * j, NB, lane));
-      mul_n<1>(F, da, ks, t0w, 16 * j, NB, lane);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j >= w) {
-        uint32_t xa[1][4];
-        ldsm4t(xa[0], block_addr(own + ring, 16 * j, lane));
-        mul_t<1, 2>(A, xa, ps, t0w, 16 * j, 128, lane);
-      }
-    const float2 eg[2] = {vec2(vec + kVecEg + t0w, 0, lane), vec2(vec + kVecEg + t0w, 1, lane)};
-    float2 be[2];
+    const uint32_t turn = lane_row(lane, 3, 4, 128) ^ ((2 * w & 7) << 4);   // columns t0w of a tile [k][t]
+    float F[kM][2][4] = {};
     {
-      float B[2][4];
-      uint32_t fa[1][4];
+      const uint32_t krow = tiles + L::kK + t0w * NB + right_row(lane, NB);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 tl = vec2(vec + kVecTail + t0w, i, lane), tau = vec2(vec + kVecTau + t0w, i, lane);
-        be[i] = vec2(vec + kVecBeta + t0w, i, lane);
+      for (int j = 0; j < N / 16; ++j) {
+        uint32_t kb[4];
+        ldsm4(kb, block(krow, j));
 #pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          F[i][r] = ka * fmaf(tl.x, F[i][r], co * A[i][r]);
-          F[i][r + 1] = ka * fmaf(tl.y, F[i][r + 1], co * A[i][r + 1]);
-          B[i][r] = F[i][r] * (be[i].x * tau.x);
-          B[i][r + 1] = F[i][r + 1] * (be[i].y * tau.y);
+        for (int m = 0; m < kM; ++m) {
+          uint32_t da[1][4];
+          ldsm4(da[0], block(Srow, j) + m * 16 * NB);
+          mul<1>(F[m][0], F[m][1], da, kb);
         }
       }
-      to_a<1>(B[0], B[1], fa);
-      stsm4(a_addr(own + L::kR, 0, t0w, 128, lane), fa[0]);
     }
-    strip_sync(strip);
+    float2 be[2], eg[2];
     {
-      float C[2][4] = {};
+      float A[kM][2][4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j >= w) {
-          uint32_t fa[1][4];
-          ldsm4(fa[0], a_addr(own + L::kR, 0, 16 * j, 128, lane));
-          mul_t<1, 2>(C, fa, ys, t0w, 16 * j, 128, lane);
+          uint32_t pb[4];
+          ldsm4t(pb, tiles + L::kP + turn + j * 2048);
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            uint32_t xa[1][4];
+            ldsm4t(xa[0], block_addr(own + ring, 16 * j, m, lane));
+            mul<1>(A[m][0], A[m][1], xa, pb);
+          }
         }
-      float W[2][4], Z[2][4];
+      float2 tl[2], bt[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float c0 = -eg[i].x * ka, c1 = -eg[i].y * ka;
-#pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          F[i][r] -= C[i][r];
-          F[i][r + 1] -= C[i][r + 1];
-          W[i][r] = F[i][r] * (be[i].x * c0);
-          W[i][r + 1] = F[i][r + 1] * (be[i].y * c1);
-          Z[i][r] = X[i][r] * eg[i].x;
-          Z[i][r + 1] = X[i][r + 1] * eg[i].y;
-        }
+        const float2 tau = vec2(vec + kVecTau + t0w, i, lane);
+        eg[i] = vec2(vec + kVecEg + t0w, i, lane);
+        tl[i] = vec2(vec + kVecTail + t0w, i, lane);
+        be[i] = vec2(vec + kVecBeta + t0w, i, lane);
+        bt[i] = make_float2(be[i].x * tau.x, be[i].y * tau.y);
       }
-      uint32_t wa[1][4];
-      to_a<1>(W[0], W[1], wa);
-      stsm4(a_addr(own + L::kW, 0, t0w, 128, lane), wa[0]);
-      to_a<1>(Z[0], Z[1], wa);
-      stsm4(a_addr(own + L::kU, 0, t0w, 128, lane), wa[0]);
-    }
-    uint32_t x[4] = {0, 0, 0, 0};
-    {
-      if (c + 1 < nc) load_x(x, c + 1);
-      const float m = fmaxf(__uint_as_float(top_of(x)) * dn, __uint_as_float(top_of<kTiles>(D)));
-      if (lane == 0) mx[4 * (c & 1) + w] = m;
-    }
-    {
-      uint8_t *to = reinterpret_cast<uint8_t *>(o.D16 + (ht * s.P + p0) * N);
 #pragma unroll
-      for (int i = 0; i < 2 * N; i += 128) {
-        const int at = 16 * (i + (threadIdx.x & 127));
-        *reinterpret_cast<uint4 *>(to + at) = *reinterpret_cast<const uint4 *>(gown + L::kS + at);
+      for (int m = 0; m < kM; ++m) {
+        uint32_t fa[1][4];
+        float B[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            F[m][i][r] = ka * fmaf(tl[i].x, F[m][i][r], co * A[m][i][r]);
+            F[m][i][r + 1] = ka * fmaf(tl[i].y, F[m][i][r + 1], co * A[m][i][r + 1]);
+            B[i][r] = F[m][i][r] * bt[i].x;
+            B[i][r + 1] = F[m][i][r + 1] * bt[i].y;
+          }
+        to_a<1>(B[0], B[1], fa);
+        stsm4(block(Rrow, w) + m * 2048, fa[0]);
       }
-      if ((threadIdx.x & 127) == 0) o.ub[(ht * s.P + p0) >> 4] = up;
     }
     strip_sync(strip);
     {
-      float Z[kTiles][4] = {};
+      float C[kM][2][4] = {};
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+      for (int j = 0; j < 4; ++j)
+        if (j >= w) {
+          uint32_t yb[4];
+          ldsm4t(yb, tiles + L::kY + turn + j * 2048);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) D[i][r] *= last;
+          for (int m = 0; m < kM; ++m) {
+            uint32_t fa[1][4];
+            ldsm4(fa[0], block(Rrow, j) + m * 2048);
+            mul<1>(C[m][0], C[m][1], fa, yb);
+          }
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t wa[1][4], ya[1][4];
-        ldsm4(wa[0], a_addr(own + L::kW, 0, 16 * j, 128, lane));
-        ldsm4(ya[0], a_addr(own + L::kU, 0, 16 * j, 128, lane));
-        mul_t<1, kTiles>(D, wa, ks, n0, 16 * j, NB, lane);
-        mul_t<1, kTiles>(Z, ya, qs, n0, 16 * j, NB, lane);
+      for (int m = 0; m < kM; ++m) {
+        uint32_t x[4], wa[1][4];
+        ldsm4t(x, block_addr(own + ring, t0w, m, lane));
+        float W[2][4], Z[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float c0 = -eg[i].x * ka, c1 = -eg[i].y * ka;
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const float2 xv = unpack(x[2 * i + r / 2]);
+            F[m][i][r] -= C[m][i][r];
+            F[m][i][r + 1] -= C[m][i][r + 1];
+            W[i][r] = F[m][i][r] * (be[i].x * c0);
+            W[i][r + 1] = F[m][i][r + 1] * (be[i].y * c1);
+            Z[i][r] = xv.x * eg[i].x;
+            Z[i][r + 1] = xv.y * eg[i].y;
+          }
+        }
+        to_a<1>(W[0], W[1], wa);
+        stsm4(block(Wrow, w) + m * 2048, wa[0]);
+        to_a<1>(Z[0], Z[1], wa);
+        stsm4(block(Urow, w) + m * 2048, wa[0]);
       }
+    }
+    {
+      float m = warp_top(top);
+      if (m < 0x1p-10f) m = state_top<kTiles>(D);   // too small for fp16 to say
+      if (c + 1 < nc) {
+        uint32_t x[kM][4];
+        load_x(x, c + 1);
+        m = fmaxf(m, rows_top(x) * sc.dn);
+      }
+      if (lane == 0) mx[4 * (c & 1) + w] = m;
+    }
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) D[i][r] = fmaf(co, Z[i][r], D[i][r]);
+        for (int r = 0; r < 4; ++r) D[m][i][r] *= last;
+    strip_sync(strip);
+    {
+      const uint32_t kcol = tiles + L::kK + ((n0 >> 6) << 7) + (lane_row(lane, 3, 4, NB) ^ ((n0 & 63) << 1));
+      // column tiles one pair after the other: the part of dO has a factor of its own
+#pragma unroll
+      for (int i = 0; i < kTiles / 2; ++i) {
+        float Z[kM][2][4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t kb[4], qb[4];
+          ldsm4t(kb, (kcol ^ (i << 5)) + j * 16 * NB);
+          ldsm4t(qb, (kcol ^ (i << 5)) + j * 16 * NB + (L::kQ - L::kK));
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            uint32_t wa[1][4], ya[1][4];
+            ldsm4(wa[0], block(Wrow, j) + m * 2048);
+            ldsm4(ya[0], block(Urow, j) + m * 2048);
+            mul<1>(D[m][2 * i], D[m][2 * i + 1], wa, kb);
+            mul<1>(Z[m][0], Z[m][1], ya, qb);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            D[m][2 * i][r] = fmaf(co, Z[m][0][r], D[m][2 * i][r]);
+            D[m][2 * i + 1][r] = fmaf(co, Z[m][1][r], D[m][2 * i + 1][r]);
+          }
+      }
     }
-    const int tok = t0w + (lane >> 1);
-    uint32_t rw[4], vw[4];
+    uint32_t rw[kM][4], vw[kM][4];
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float f0 = F[m][i][2 * r], f1 = F[m][i][2 * r + 1];
+          rw[m][2 * i + r] = pack(f0, f1);
+          vw[m][2 * i + r] = pack_bf16(f0 * (be[i].x * sc.up), f1 * (be[i].y * sc.up));
+        }
+    const int col = 8 * (lane & 3);
+    const int64_t at = (ht * kChunk + t0w + (lane >> 2)) * s.P + p0 + col;
+    uint4 out[2];
+    // every warp has read dO's tiles by the last barrier: this warp's tokens of the block are its own
 #pragma unroll
     for (int i = 0; i < 2; ++i)
+      if (col < rows)
+        *reinterpret_cast<uint4 *>(o.X16 + at + 8 * i * s.P) =
+            *reinterpret_cast<const uint4 *>(gown + ring + row_at(t0w + 8 * i + (lane >> 2), lane & 3));
+    turned(out, gown + ring, own + ring, rw, t0w, lane);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        rw[2 * i + r] = pack(F[i][2 * r], F[i][2 * r + 1]);
-        vw[2 * i + r] = pack_bf16(F[i][2 * r] * (be[i].x * up), F[i][2 * r + 1] * (be[i].y * up));
-      }
-    const int64_t at = (ht * kChunk + tok) * s.P + p0 + 8 * (lane & 1);
-    *reinterpret_cast<uint4 *>(o.X16 + at) = *reinterpret_cast<const uint4 *>(gown + ring + row_at(tok, lane & 1));
-    *reinterpret_cast<uint4 *>(o.F16 + at) = turned(gown + ring, own + ring, rw, t0w, lane);
-    const uint4 vv = turned(gown + ring, own + ring, vw, t0w, lane);
-    if (tok < ck.n) put_out(dv + (ck.b + tok) * tok_stride + h * s.P + p0 + 8 * (lane & 1), ovec, vv);
-    move(rescale(strip_top(mx + 4 * (c & 1)), dn));
-    if (c + 1 < nc) take_x(x, c + 1);
+    for (int i = 0; i < 2; ++i)
+      if (col < rows) *reinterpret_cast<uint4 *>(o.F16 + at + 8 * i * s.P) = out[i];
+    turned(out, gown + ring, own + ring, vw, t0w, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tok = t0w + 8 * i + (lane >> 2);
+      if (tok < ck.n && col < rows) put_out(dv + (ck.b + tok) * tok_stride + h * s.P + p0 + col, ovec, out[i]);
+    }
+    sc.move(D, rescale(strip_top(mx + 4 * (c & 1)), sc.dn));
+    if (c + 1 < nc) {
+      uint32_t x[kM][4];
+      load_x(x, c + 1);
+      take_x(x, c + 1);
+    }
   }
-  cp_wait<0>();
-  if (live && a.dinit != nullptr) store_state<kTiles>(D, a.dinit + row, up, N, lane);
+  if (live && a.dinit != nullptr) store_state<kTiles>(D, a.dinit + row, sc.up, rows, N, lane);
 }
 
 bool vec16(const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; }
 
-// Strips of a CTA: several share one copy of the chunk's tiles, fewer spread over more SMs.  At most `most`, and
-// only while that still gives 120 of the 152 SMs a CTA.
-int strips_of(const Shape &s, int most) {
-  const int strips = (s.P + 15) / 16;
-  int n = most;
-  while (n > 1 && (n >= 2 * strips || s.nseq * s.H * ((strips + n - 1) / n) < 120)) n /= 2;
-  return n;
+// Strips of a CTA: two share one copy of the chunk's tiles, one each spread over more SMs; two while that still gives
+// 120 of the 152 SMs a CTA.  (Four strips leave 96 registers a thread: 260 us in place of 222 for 2048 tokens x 128 heads.)
+int strips_of(const Shape &s) {
+  const int strips = (s.P + kRows - 1) / kRows;
+  return strips > 1 && s.nseq * s.H * ((strips + 1) / 2) >= 120 ? 2 : 1;
 }
 dim3 chain_grid(const Shape &s, int n) {
-  return dim3(unsigned(((s.P + 15) / 16 + n - 1) / n), unsigned(s.H), unsigned(s.nseq));
+  return dim3(unsigned(((s.P + kRows - 1) / kRows + n - 1) / n), unsigned(s.H), unsigned(s.nseq));
 }
 
 template <int N, int kTerms, int kStrips, bool kSave>
 cudaError_t go_fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
   auto kernel = chain_fwd_kernel<N, kTerms, kStrips, kSave>;
-  constexpr int smem = Layout<N, kTerms>::bytes(kStrips);
+  constexpr int smem = Layout<N, kTerms, kStrips>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<chain_grid(s, kStrips), 128 * kStrips, smem, st>>>(s, a, t, vec16(a.v, s.vs), vec16(a.o, 8));
+  kernel<<<chain_grid(s, kStrips), 128 * kStrips + kLoaders, smem, st>>>(s, a, t, vec16(a.v, s.vs), vec16(a.o, 8));
   return cudaGetLastError();
 }
 
 template <int N, int kTerms, bool kSave>
 cudaError_t pick_fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
-  // four strips with two terms would need more shared memory than an SM has
-  const int n = strips_of(s, kTerms == 2 && N == 128 ? 2 : 4);
-  if constexpr (kTerms == 1 || N == 64)
-    if (n == 4) return go_fwd<N, kTerms, 4, kSave>(s, a, t, st);
-  return n >= 2 ? go_fwd<N, kTerms, 2, kSave>(s, a, t, st) : go_fwd<N, kTerms, 1, kSave>(s, a, t, st);
+  return strips_of(s) == 2 ? go_fwd<N, kTerms, 2, kSave>(s, a, t, st) : go_fwd<N, kTerms, 1, kSave>(s, a, t, st);
 }
 
 template <int N>
@@ -718,17 +884,16 @@ cudaError_t fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) 
 template <int N, int kStrips>
 cudaError_t go_bwd(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st) {
   auto kernel = chain_bwd_kernel<N, kStrips>;
-  constexpr int smem = Layout<N, 1>::bytes(kStrips);
+  constexpr int smem = Layout<N, 1, kStrips>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<chain_grid(s, kStrips), 128 * kStrips, smem, st>>>(s, a, t, b, vec16(a.dout, 8), vec16(a.dv, 8));
+  kernel<<<chain_grid(s, kStrips), 128 * kStrips + kLoaders, smem, st>>>(s, a, t, b, vec16(a.dout, 8), vec16(a.dv, 8));
   return cudaGetLastError();
 }
 
 template <int N>
 cudaError_t bwd(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st) {
-  const int n = strips_of(s, 4);
-  return n == 4 ? go_bwd<N, 4>(s, a, t, b, st) : n == 2 ? go_bwd<N, 2>(s, a, t, b, st) : go_bwd<N, 1>(s, a, t, b, st);
+  return strips_of(s) == 2 ? go_bwd<N, 2>(s, a, t, b, st) : go_bwd<N, 1>(s, a, t, b, st);
 }
 
 }  // namespace
