@@ -70,10 +70,13 @@ struct Chunk {
 
 // Byte offset of 16-byte piece j (of four) of token t in a strip's 64 x 32 block.
 __device__ __forceinline__ uint32_t row_at(int t, int j) { return t * 64 + ((j ^ ((t >> 1) & 3)) << 4); }
-// This lane's row of a transposing load or store of 16 tokens x 16 rows (4 matrices) of a block: accumulator layout,
-// tokens as columns.
-__device__ __forceinline__ uint32_t block_addr(uint32_t block, int t0, int m, int lane) {
-  return block + row_at(t0 + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1));
+// A warp's tokens are two tiles of eight, number w and 7 - w of the chunk's: triangular products then cost each of the
+// four warps the same.
+__device__ __forceinline__ int tile_of(int w, int i) { return i ? 7 - w : w; }
+// This lane's row of a transposing load or store of two tiles of 8 tokens x 16 rows (4 matrices) of a block:
+// accumulator layout, tokens as columns.
+__device__ __forceinline__ uint32_t block_addr(uint32_t block, int tile0, int tile1, int m, int lane) {
+  return block + row_at(8 * (lane >> 4 ? tile1 : tile0) + (lane & 7), 2 * m + ((lane >> 3) & 1));
 }
 
 __device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
@@ -83,13 +86,20 @@ __device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ void strip_sync(int strip) { asm volatile("bar.sync %0, 128;" ::"r"(strip + 1) : "memory"); }
 
-// Where a lane's row of a four-matrix load or store begins, for 16 x 16 block 0 of its tile; `block` gives block j
-// along the rows (tiles are aligned to 128 bytes, so the swizzle is an exclusive or of the address itself).
-__device__ __forceinline__ uint32_t lane_row(int lane, int hi_row, int hi_col, int bytes) {   // bits of lane: +8 rows, +8 columns
-  return ((lane & 7) + (((lane >> hi_row) & 1) << 3)) * bytes + (((((lane >> hi_col) & 1)) ^ (lane & 7)) << 4);
+// Where a lane's row of a four-matrix load or store begins.  Tiles are aligned to 128 bytes, so the swizzle is an
+// exclusive or of the address itself, and `block` gives the row's 16 columns number j.
+//   left_row: 16 x 16 at (0, 0), the matrices' rows first
+__device__ __forceinline__ uint32_t left_row(int lane, int bytes) {
+  return ((lane & 7) + (lane & 8)) * bytes + (((lane >> 4) ^ (lane & 7)) << 4);
 }
-__device__ __forceinline__ uint32_t left_row(int lane, int bytes) { return lane_row(lane, 3, 4, bytes); }
-__device__ __forceinline__ uint32_t right_row(int lane, int bytes) { return lane_row(lane, 4, 3, bytes); }   // tile [n][k]
+//   right_row: the warp's two tiles of tokens as rows
+__device__ __forceinline__ uint32_t right_row(int w, int lane, int bytes) {
+  return (8 * tile_of(w, lane >> 4) + (lane & 7)) * bytes + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+}
+//   turned_row: 16 rows, the warp's two tiles of tokens as columns, rows of 128 bytes
+__device__ __forceinline__ uint32_t turned_row(int w, int lane) {
+  return ((lane & 7) + (lane & 8)) * 128 + ((tile_of(w, lane >> 4) ^ (lane & 7)) << 4);
+}
 __device__ __forceinline__ uint32_t block(uint32_t row, int j) { return (row ^ ((j & 3) << 5)) + ((j >> 2) << 7); }
 
 // 16 x 16 values (two accumulator tiles) rounded, as the four matrices of a store.
@@ -151,7 +161,14 @@ __device__ __forceinline__ void fetch_rows(const Chunk &c, const __nv_bfloat16 *
   }
 }
 
-// What the copying warps do: the tiles of a chunk and the rows of the one after, a stage or two ahead.
+// Largest magnitude of bf16 pairs, a warp's (NaN counts for more than any number).
+__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7fff7fffu); }
+__device__ __forceinline__ float bf16_top(uint32_t m) {
+  return __uint_as_float(__reduce_max_sync(~0u, max(m & 0xffffu, m >> 16)) << 16);
+}
+
+// What the copying warps do: the tiles of a chunk and the rows of the one after, a stage or two ahead, and each
+// strip's largest value of those rows, for which the chain would have to wait.
 template <int N, int kTerms, int kStrips, int kThreads, class Of>
 __device__ __forceinline__ void copy_in(const Shape &s, const Tiles &t, const __nv_bfloat16 *x, int64_t stride, bool vec,
                                         int h, int p0, int64_t nc, Of of, uint8_t *smem, int tid) {
@@ -164,6 +181,22 @@ __device__ __forceinline__ void copy_in(const Shape &s, const Tiles &t, const __
       fetch_rows<kStrips, kThreads>(of(c), x + h * s.P, stride, p0, s.P, vec, base + at, smem + at, L::kStrip, tid);
     }
   };
+  auto tops = [&](int64_t c) {   // of the pieces that this thread has copied
+#pragma unroll
+    for (int y = 0; y < kStrips; ++y) {
+      uint32_t m = 0;
+      if (c < nc)
+#pragma unroll
+        for (int i = 0; i < 256; i += kThreads) {
+          const int r = (i + tid) >> 2, j = tid & 3;
+          const uint4 v = *reinterpret_cast<const uint4 *>(smem + kOwn + y * L::kStrip + int(c % L::kRing) * kBlock + row_at(r, j));
+          m = top2(top2(top2(top2(m, v.x), v.y), v.z), v.w);
+        }
+      const float top = bf16_top(m);
+      if ((tid & 31) == 0)
+        reinterpret_cast<float *>(smem + kOwn + y * L::kStrip + L::kMax)[8 + 4 * int(c & 1) + (tid >> 5)] = top;
+    }
+  };
   auto fetch = [&](int64_t c) {
     if (c < nc) fetch_tiles<N, kTerms, kStrips, kThreads>(s, t, of(c).slot, h, base + int(c % L::kStages) * L::kStage, tid);
     rows(c + 1);
@@ -174,9 +207,11 @@ __device__ __forceinline__ void copy_in(const Shape &s, const Tiles &t, const __
   cp_commit();
   for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
   cp_wait<L::kStages - 1>();
+  tops(0);
   __syncthreads();
   for (int64_t c = 0; c < nc; ++c) {
     cp_wait<L::kStages - 2>();
+    tops(c + 1);
     __syncthreads();   // tiles of c, rows of c + 1 are here; everyone is done with chunk c - 1
     fetch(c + L::kStages - 1);
   }
@@ -196,31 +231,22 @@ __device__ __forceinline__ void put_out(__nv_bfloat16 *p, bool vec, uint4 v) {
   }
 }
 
-// This warp's 16 tokens x 32 rows through its part of a block to [token][row]: pieces lane and lane + 32 of 16 bytes.
-__device__ __forceinline__ void turned(uint4 (&v)[2], uint8_t *gblock, uint32_t blk, const uint32_t (&w)[kM][4], int t0,
+// This warp's 16 tokens x 32 rows through its part of a block to [token][row]: the lane's 16 bytes of either tile.
+__device__ __forceinline__ void turned(uint4 (&v)[2], uint8_t *gblock, uint32_t blk, const uint32_t (&x)[kM][4], int w,
                                        int lane) {
   __syncwarp();
 #pragma unroll
-  for (int m = 0; m < kM; ++m) stsm4t(block_addr(blk, t0, m, lane), w[m]);
+  for (int m = 0; m < kM; ++m) stsm4t(block_addr(blk, w, 7 - w, m, lane), x[m]);
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    v[i] = *reinterpret_cast<const uint4 *>(gblock + row_at(t0 + 8 * i + (lane >> 2), lane & 3));
+    v[i] = *reinterpret_cast<const uint4 *>(gblock + row_at(8 * tile_of(w, i) + (lane >> 2), lane & 3));
 }
 
-// Largest magnitude of a warp's packed fp16 (NaN counts for more than any number).
+// Largest magnitude of a warp's packed fp16.
 __device__ __forceinline__ float warp_top(uint32_t m) {
-  const uint32_t u = __reduce_max_sync(~0u, max(m & 0x7fffu, (m >> 16) & 0x7fffu));
+  const uint32_t u = __reduce_max_sync(~0u, max(m & 0xffffu, m >> 16));
   return __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
-}
-// The larger of each half's magnitude.
-__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7fff7fffu); }
-// Largest magnitude of a warp's bf16 pairs.
-__device__ __forceinline__ float rows_top(const uint32_t (&w)[kM][4]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4 * kM; ++i) m = top2(m, w[i / 4][i % 4]);
-  return __uint_as_float(__reduce_max_sync(~0u, max(m & 0x7fffu, m >> 16)) << 16);
 }
 template <int kTiles>
 __device__ __forceinline__ float state_top(const float (&S)[kM][kTiles][4]) {
@@ -243,9 +269,10 @@ __device__ __forceinline__ float rescale(float need, float dn) {
   const float lim = 1.0e33f;   // keeps both scales finite
   return dn * f > lim || dn * f < 1.f / lim ? 1.f : f;
 }
+// Four warps' largest values.  The larger as bits: a NaN stays one.
 __device__ __forceinline__ float strip_top(const float *mx) {
-  const float4 v = *reinterpret_cast<const float4 *>(mx);
-  return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+  const uint4 v = *reinterpret_cast<const uint4 *>(mx);
+  return __uint_as_float(max(max(v.x, v.y), max(v.z, v.w)));
 }
 
 // A strip's running scale: values are held times `dn` = 1 / `up`.
@@ -294,17 +321,19 @@ __device__ __forceinline__ void store_state(const float (&S)[kM][kTiles][4], flo
               make_float2(S[m][i][2 * r] * up, S[m][i][2 * r + 1] * up);
 }
 
-__device__ __forceinline__ float2 vec2(const float *v, int i, int lane) {
-  return *reinterpret_cast<const float2 *>(v + 8 * i + 2 * (lane & 3));
+// This lane's pair of a vector over tokens, in tile i of its warp's.
+__device__ __forceinline__ float2 vec2(const float *v, int w, int i, int lane) {
+  return *reinterpret_cast<const float2 *>(v + 8 * tile_of(w, i) + 2 * (lane & 3));
 }
 
-// Two neighbouring accumulator tiles of each of the strip's products += its left operands a times one right operand.
-template <int kTerms>
-__device__ __forceinline__ void mul(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[kTerms][4], const uint32_t (&b)[4]) {
+// The strip's products of one pair of accumulator tiles += left operands times one right operand.
+template <int kT>
+__device__ __forceinline__ void mul(float (&d)[kM][kT][4], int i0, const uint32_t (&a)[kM][4], const uint32_t (&b)[4],
+                                    bool first = true, bool second = true) {
 #pragma unroll
-  for (int t = 0; t < kTerms; ++t) {
-    mma(d0, a[t], b[0], b[1]);
-    mma(d1, a[t], b[2], b[3]);
+  for (int m = 0; m < kM; ++m) {
+    if (first) mma(d[m][i0], a[m], b[0], b[1]);
+    if (second) mma(d[m][i0 + 1], a[m], b[2], b[3]);
   }
 }
 
@@ -342,7 +371,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
   constexpr int kTiles = N / 32, NB = 2 * N;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
-  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * kRows, n0 = w * (N / 4), t0w = 16 * w;
+  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * kRows, n0 = w * (N / 4);
   const int64_t seq = blockIdx.z;
   int64_t t0, te;
   seq_range(s, a.cu, seq, t0, te);
@@ -362,7 +391,9 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
   uint8_t *gown = smem + L::kStages * L::kStage + strip * L::kStrip;
   float *mx = reinterpret_cast<float *>(gown + L::kMax);
   const uint32_t Srow = own + L::kS + left_row(lane, NB), Rrow = own + L::kR + left_row(lane, 128),
-                 Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128);
+                 Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128),
+                 Rput = own + L::kR + turned_row(w, lane), Uput = own + L::kU + turned_row(w, lane),
+                 Wput = own + L::kW + turned_row(w, lane);
   float S[kM][kTiles][4];
   Scaled<kTiles> sc;
   const int64_t row = ((seq * s.H + h) * s.P + p0) * N + n0;
@@ -370,17 +401,15 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
   // v of chunk c, this warp's tokens, as packed pairs
   auto load_v = [&](uint32_t (&x)[kM][4], int64_t c) {
 #pragma unroll
-    for (int m = 0; m < kM; ++m) ldsm4t(x[m], block_addr(own + int(c % L::kRing) * kBlock, t0w, m, lane));
+    for (int m = 0; m < kM; ++m) ldsm4t(x[m], block_addr(own + int(c % L::kRing) * kBlock, w, 7 - w, m, lane));
   };
   if (nc > 0) {
     __syncthreads();
     if (live) {
-      uint32_t x[kM][4];
-      load_v(x, 0);
-      const float m = fmaxf(rows_top(x), state_top<kTiles>(S));
+      const float m = state_top<kTiles>(S);
       if (lane == 0) mx[4 + w] = m;
       strip_sync(strip);
-      sc.move(S, rescale(strip_top(mx + 4), 1.f));
+      sc.move(S, rescale(fmaxf(strip_top(mx + 4), strip_top(mx + 8)), 1.f));
     }
   }
   for (int64_t c = 0; c < nc; ++c) {
@@ -399,25 +428,22 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
     const uint32_t tiles = base + stage;
     const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
     const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1];
-    const float2 eg[2] = {vec2(vec + kVecEg + t0w, 0, lane), vec2(vec + kVecEg + t0w, 1, lane)};
+    const float2 eg[2] = {vec2(vec + kVecEg, w, 0, lane), vec2(vec + kVecEg, w, 1, lane)};
     float R[kM][2][4] = {}, O[kM][2][4] = {};
     {
-      const uint32_t krow = tiles + L::kK + t0w * NB + right_row(lane, NB);
+      const uint32_t krow = tiles + L::kK + right_row(w, lane, NB);
 #pragma unroll
       for (int j = 0; j < N / 16; ++j) {
-        uint32_t sa[kM][kTerms][4], kb[4], qb[4];
+        uint32_t sa[kTerms][kM][4], kb[4], qb[4];
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+        for (int i = 0; i < kTerms; ++i)
 #pragma unroll
-          for (int i = 0; i < kTerms; ++i) ldsm4(sa[m][i], block(Srow, j) + m * 16 * NB + i * L::kPlane);
+          for (int m = 0; m < kM; ++m) ldsm4(sa[i][m], block(Srow, j) + m * 16 * NB + i * L::kPlane);
         ldsm4(kb, block(krow, j));
         ldsm4(qb, block(krow, j) + (L::kQ - L::kK));
-#pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          mul<kTerms>(R[m][0], R[m][1], sa[m], kb);
-          mma(O[m][0], sa[m][0], qb[0], qb[1]);
-          mma(O[m][1], sa[m][0], qb[2], qb[3]);
-        }
+        mul(R, 0, sa[0], kb);   // an accumulator's products four or more apart
+        mul(O, 0, sa[0], qb);
+        if (kTerms == 2) mul(R, 0, sa[kTerms - 1], kb);
       }
     }
     float2 be[2];
@@ -425,7 +451,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
       uint32_t vw[kM][4];
       load_v(vw, c);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) be[i] = vec2(vec + kVecBeta + t0w, i, lane);
+      for (int i = 0; i < 2; ++i) be[i] = vec2(vec + kVecBeta, w, i, lane);
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         float B[2][4];
@@ -444,38 +470,44 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         }
         to_a<kTerms>(B[0], B[1], ra);
 #pragma unroll
-        for (int i = 0; i < kTerms; ++i) stsm4(block(Rrow, w) + m * 2048 + i * L::kRow, ra[i]);
+        for (int i = 0; i < kTerms; ++i) stsm4(Rput + m * 2048 + i * L::kRow, ra[i]);
       }
     }
     strip_sync(strip);
     uint32_t ew[kM][4];
     {
-      float E[kM][2][4] = {};
-      const uint32_t yrow = tiles + L::kY + t0w * 128 + right_row(lane, 128);
+      float E[kM][2][4] = {}, E2[kM][2][4] = {};   // E2: of the second terms, where registers allow it
+      constexpr bool kApart = kTerms == 2 && kStrips == 1;
+      const uint32_t yrow = tiles + L::kY + right_row(w, lane, 128);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-          uint32_t ra[kM][kTerms][4], yb[kTerms][4];
+      for (int j = 0; j < 4; ++j) {
+        // Y and P are zero above the diagonal.  A warp of its own on a scheduler does better with a product too many
+        // (the first tile's tokens are below 32) than with branches, two warps with only what they need.
+        if (kStrips > 1 && 2 * j > 7 - w) break;
+        uint32_t ra[kTerms][kM][4], yb[kTerms][4];
 #pragma unroll
-          for (int i = 0; i < kTerms; ++i) {
+        for (int i = 0; i < kTerms; ++i) {
 #pragma unroll
-            for (int m = 0; m < kM; ++m) ldsm4(ra[m][i], block(Rrow, j) + m * 2048 + i * L::kRow);
-            ldsm4(yb[i], block(yrow, j) + i * 8192);
-          }
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            mul<kTerms>(E[m][0], E[m][1], ra[m], yb[0]);
-            if (kTerms == 2) {
-              mma(E[m][0], ra[m][0], yb[kTerms - 1][0], yb[kTerms - 1][1]);
-              mma(E[m][1], ra[m][0], yb[kTerms - 1][2], yb[kTerms - 1][3]);
-            }
-          }
+          for (int m = 0; m < kM; ++m) ldsm4(ra[i][m], block(Rrow, j) + m * 2048 + i * L::kRow);
+          ldsm4(yb[i], block(yrow, j) + i * 8192);
         }
+        const bool on = kStrips > 1 ? 2 * j <= w : j < 2;
+        mul(E, 0, ra[0], yb[0], on);
+        if (kTerms == 2) {
+          mul(kApart ? E2 : E, 0, ra[kTerms - 1], yb[0], on);
+          mul(kApart ? E2 : E, 0, ra[0], yb[kTerms - 1], on);
+        }
+      }
+      if (kApart)
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) E[m][i / 4][i % 4] += E2[m][i / 4][i % 4];
       float2 tau[2], tl[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        tau[i] = vec2(vec + kVecTau + t0w, i, lane);
-        tl[i] = vec2(vec + kVecTail + t0w, i, lane);
+        tau[i] = vec2(vec + kVecTau, w, i, lane);
+        tl[i] = vec2(vec + kVecTail, w, i, lane);
       }
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
@@ -494,20 +526,15 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         uint32_t ua[1][4], wa[kTerms][4];
         to_a<kTerms>(W[0], W[1], wa);
 #pragma unroll
-        for (int i = 0; i < kTerms; ++i) stsm4(block(Wrow, w) + m * 2048 + i * L::kRow, wa[i]);
+        for (int i = 0; i < kTerms; ++i) stsm4(Wput + m * 2048 + i * L::kRow, wa[i]);
         to_a<1>(E[m][0], E[m][1], ua);
-        stsm4(block(Urow, w) + m * 2048, ua[0]);
+        stsm4(Uput + m * 2048, ua[0]);
       }
     }
     {
-      // the next chunk's scale: its rows, and this chunk's state (which one chunk cannot carry out of fp16's range)
+      // this chunk's state, for the next one's scale (one chunk cannot carry it out of fp16's range)
       float m = warp_top(top);
       if (m < 0x1p-10f) m = state_top<kTiles>(S);   // too small for fp16 to say
-      if (c + 1 < nc) {
-        uint32_t x[kM][4];
-        load_v(x, c + 1);
-        m = fmaxf(m, rows_top(x) * sc.dn);
-      }
       if (lane == 0) mx[4 * (c & 1) + w] = m;
     }
 #pragma unroll
@@ -526,38 +553,35 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
           O[m][i][r + 1] *= eg[i].y;
         }
     strip_sync(strip);
+    const float f = rescale(fmaxf(strip_top(mx + 4 * (c & 1)), strip_top(mx + 8 + 4 * ((c + 1) & 1)) * sc.dn), sc.dn);
     {
-      const uint32_t kcol = tiles + L::kK + ((n0 >> 6) << 7) + (lane_row(lane, 3, 4, NB) ^ ((n0 & 63) << 1));
+      const uint32_t kcol = tiles + L::kK + block(left_row(lane, NB), n0 >> 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t wa[kM][kTerms][4];
+        uint32_t wa[kTerms][kM][4], kb[kTiles / 2][4];
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+        for (int i = 0; i < kTerms; ++i)
 #pragma unroll
-          for (int i = 0; i < kTerms; ++i) ldsm4(wa[m][i], block(Wrow, j) + m * 2048 + i * L::kRow);
+          for (int m = 0; m < kM; ++m) ldsm4(wa[i][m], block(Wrow, j) + m * 2048 + i * L::kRow);
 #pragma unroll
-        for (int i = 0; i < kTiles / 2; ++i) {
-          uint32_t kb[4];
-          ldsm4t(kb, (kcol ^ (i << 5)) + j * 16 * NB);
+        for (int i = 0; i < kTiles / 2; ++i) ldsm4t(kb[i], (kcol ^ (i << 5)) + j * 16 * NB);
 #pragma unroll
-          for (int m = 0; m < kM; ++m) mul<kTerms>(S[m][2 * i], S[m][2 * i + 1], wa[m], kb);
-        }
+        for (int x = 0; x < kTerms; ++x)
+#pragma unroll
+          for (int i = 0; i < kTiles / 2; ++i) mul(S, 2 * i, wa[x], kb[i]);
       }
     }
     {
-      const uint32_t prow = tiles + L::kP + t0w * 128 + right_row(lane, 128);
+      const uint32_t prow = tiles + L::kP + right_row(w, lane, 128);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-          uint32_t pb[4];
-          ldsm4(pb, block(prow, j));
+      for (int j = 0; j < 4; ++j) {
+        if (kStrips > 1 && 2 * j > 7 - w) break;
+        uint32_t pb[4], ua[kM][4];
+        ldsm4(pb, block(prow, j));
 #pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            uint32_t ua[1][4];
-            ldsm4(ua[0], block(Urow, j) + m * 2048);
-            mul<1>(O[m][0], O[m][1], ua, pb);
-          }
-        }
+        for (int m = 0; m < kM; ++m) ldsm4(ua[m], block(Urow, j) + m * 2048);
+        mul(O, 0, ua, pb, kStrips > 1 ? 2 * j <= w : j < 2);
+      }
     }
     // outputs and record through this warp's tokens of the v block, which it alone has read
     const float co = a.scale * ka * sc.up;
@@ -567,21 +591,21 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) ow[m][i] = pack_bf16(O[m][i >> 1][2 * (i & 1)] * co, O[m][i >> 1][2 * (i & 1) + 1] * co);
     uint4 out[2];
-    turned(out, gown + ring, own + ring, ow, t0w, lane);
+    turned(out, gown + ring, own + ring, ow, w, lane);
     const int col = 8 * (lane & 3);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tok = t0w + 8 * i + (lane >> 2);
+      const int tok = 8 * tile_of(w, i) + (lane >> 2);
       if (tok < ck.n && col < rows) put_out(o + ((ck.b + tok) * s.H + h) * s.P + p0 + col, ovec, out[i]);
     }
     if (kSave) {
-      turned(out, gown + ring, own + ring, ew, t0w, lane);
+      turned(out, gown + ring, own + ring, ew, w, lane);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (col < rows)
-          *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + t0w + 8 * i + (lane >> 2)) * s.P + p0 + col) = out[i];
+          *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + 8 * tile_of(w, i) + (lane >> 2)) * s.P + p0 + col) = out[i];
     }
-    sc.move(S, rescale(strip_top(mx + 4 * (c & 1)), sc.dn));
+    sc.move(S, f);
   }
   if (live && a.fin != nullptr) store_state<kTiles>(S, a.fin + row, sc.up, rows, N, lane);
 }
@@ -594,7 +618,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
   constexpr int kTiles = N / 32, NB = 2 * N;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
-  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * kRows, n0 = w * (N / 4), t0w = 16 * w;
+  const int h = blockIdx.y, p0 = (blockIdx.x * kStrips + strip) * kRows, n0 = w * (N / 4);
   const int64_t seq = blockIdx.z, tok_stride = int64_t(s.H) * s.P;
   int64_t t0, te;
   seq_range(s, a.cu, seq, t0, te);
@@ -616,38 +640,36 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
   uint8_t *gown = smem + L::kStages * L::kStage + strip * L::kStrip;
   float *mx = reinterpret_cast<float *>(gown + L::kMax);
   const uint32_t Srow = own + L::kS + left_row(lane, NB), Rrow = own + L::kR + left_row(lane, 128),
-                 Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128);
+                 Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128),
+                 Rput = own + L::kR + turned_row(w, lane), Uput = own + L::kU + turned_row(w, lane),
+                 Wput = own + L::kW + turned_row(w, lane);
   float D[kM][kTiles][4];
   Scaled<kTiles> sc;
   const int64_t row = ((seq * s.H + h) * s.P + p0) * N + n0;
   load_state<kTiles>(D, a.dfinal + row, a.dfinal != nullptr ? rows : 0, N, lane);
   // dO of this warp's tokens in units of the strip's scale: as fp16 it takes the place of dO in the ring
-  auto take_x = [&](const uint32_t (&x)[kM][4], int64_t c) {
+  auto take_x = [&](int64_t c) {
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
-      uint32_t xa[4];
+      const uint32_t at = block_addr(own + int(c % L::kRing) * kBlock, w, 7 - w, m, lane);
+      uint32_t x[4];
+      ldsm4t(x, at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack_bf16(x[m][i]);
-        xa[i] = pack(v.x * sc.dn, v.y * sc.dn);
+        const float2 v = unpack_bf16(x[i]);
+        x[i] = pack(v.x * sc.dn, v.y * sc.dn);
       }
-      stsm4t(block_addr(own + int(c % L::kRing) * kBlock, t0w, m, lane), xa);
+      stsm4t(at, x);
     }
-  };
-  auto load_x = [&](uint32_t (&x)[kM][4], int64_t c) {
-#pragma unroll
-    for (int m = 0; m < kM; ++m) ldsm4t(x[m], block_addr(own + int(c % L::kRing) * kBlock, t0w, m, lane));
   };
   if (nc > 0) {
     __syncthreads();
     if (live) {
-      uint32_t x[kM][4];
-      load_x(x, 0);
-      const float m = fmaxf(rows_top(x), state_top<kTiles>(D));
+      const float m = state_top<kTiles>(D);
       if (lane == 0) mx[4 + w] = m;
       strip_sync(strip);
-      sc.move(D, rescale(strip_top(mx + 4), 1.f));
-      take_x(x, 0);
+      sc.move(D, rescale(fmaxf(strip_top(mx + 4), strip_top(mx + 8)), 1.f));
+      take_x(0);
     }
   }
   for (int64_t c = 0; c < nc; ++c) {
@@ -664,44 +686,37 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
     const uint32_t tiles = base + stage;
     const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
     const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1], co = a.scale * ka;
-    const uint32_t turn = lane_row(lane, 3, 4, 128) ^ ((2 * w & 7) << 4);   // columns t0w of a tile [k][t]
+    const uint32_t turn = turned_row(w, lane);
     float F[kM][2][4] = {};
     {
-      const uint32_t krow = tiles + L::kK + t0w * NB + right_row(lane, NB);
+      const uint32_t krow = tiles + L::kK + right_row(w, lane, NB);
 #pragma unroll
       for (int j = 0; j < N / 16; ++j) {
-        uint32_t kb[4];
+        uint32_t kb[4], da[kM][4];
         ldsm4(kb, block(krow, j));
 #pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          uint32_t da[1][4];
-          ldsm4(da[0], block(Srow, j) + m * 16 * NB);
-          mul<1>(F[m][0], F[m][1], da, kb);
-        }
+        for (int m = 0; m < kM; ++m) ldsm4(da[m], block(Srow, j) + m * 16 * NB);
+        mul(F, 0, da, kb);
       }
     }
     float2 be[2], eg[2];
     {
       float A[kM][2][4] = {};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j >= w) {
-          uint32_t pb[4];
-          ldsm4t(pb, tiles + L::kP + turn + j * 2048);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t pb[4], xa[kM][4];
+        ldsm4t(pb, tiles + L::kP + turn + j * 2048);
 #pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            uint32_t xa[1][4];
-            ldsm4t(xa[0], block_addr(own + ring, 16 * j, m, lane));
-            mul<1>(A[m][0], A[m][1], xa, pb);
-          }
-        }
+        for (int m = 0; m < kM; ++m) ldsm4t(xa[m], block_addr(own + ring, 2 * j, 2 * j + 1, m, lane));
+        mul(A, 0, xa, pb, true, j >= 2);   // the second tile's tokens are from 32 on
+      }
       float2 tl[2], bt[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 tau = vec2(vec + kVecTau + t0w, i, lane);
-        eg[i] = vec2(vec + kVecEg + t0w, i, lane);
-        tl[i] = vec2(vec + kVecTail + t0w, i, lane);
-        be[i] = vec2(vec + kVecBeta + t0w, i, lane);
+        const float2 tau = vec2(vec + kVecTau, w, i, lane);
+        eg[i] = vec2(vec + kVecEg, w, i, lane);
+        tl[i] = vec2(vec + kVecTail, w, i, lane);
+        be[i] = vec2(vec + kVecBeta, w, i, lane);
         bt[i] = make_float2(be[i].x * tau.x, be[i].y * tau.y);
       }
 #pragma unroll
@@ -718,28 +733,24 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
             B[i][r + 1] = F[m][i][r + 1] * bt[i].y;
           }
         to_a<1>(B[0], B[1], fa);
-        stsm4(block(Rrow, w) + m * 2048, fa[0]);
+        stsm4(Rput + m * 2048, fa[0]);
       }
     }
     strip_sync(strip);
     {
       float C[kM][2][4] = {};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j >= w) {
-          uint32_t yb[4];
-          ldsm4t(yb, tiles + L::kY + turn + j * 2048);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t yb[4], fa[kM][4];
+        ldsm4t(yb, tiles + L::kY + turn + j * 2048);
 #pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            uint32_t fa[1][4];
-            ldsm4(fa[0], block(Rrow, j) + m * 2048);
-            mul<1>(C[m][0], C[m][1], fa, yb);
-          }
-        }
+        for (int m = 0; m < kM; ++m) ldsm4(fa[m], block(Rrow, j) + m * 2048);
+        mul(C, 0, fa, yb, true, j >= 2);
+      }
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         uint32_t x[4], wa[1][4];
-        ldsm4t(x, block_addr(own + ring, t0w, m, lane));
+        ldsm4t(x, block_addr(own + ring, w, 7 - w, m, lane));
         float W[2][4], Z[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -756,19 +767,14 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
           }
         }
         to_a<1>(W[0], W[1], wa);
-        stsm4(block(Wrow, w) + m * 2048, wa[0]);
+        stsm4(Wput + m * 2048, wa[0]);
         to_a<1>(Z[0], Z[1], wa);
-        stsm4(block(Urow, w) + m * 2048, wa[0]);
+        stsm4(Uput + m * 2048, wa[0]);
       }
     }
     {
       float m = warp_top(top);
       if (m < 0x1p-10f) m = state_top<kTiles>(D);   // too small for fp16 to say
-      if (c + 1 < nc) {
-        uint32_t x[kM][4];
-        load_x(x, c + 1);
-        m = fmaxf(m, rows_top(x) * sc.dn);
-      }
       if (lane == 0) mx[4 * (c & 1) + w] = m;
     }
 #pragma unroll
@@ -778,34 +784,33 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
 #pragma unroll
         for (int r = 0; r < 4; ++r) D[m][i][r] *= last;
     strip_sync(strip);
+    const float f = rescale(fmaxf(strip_top(mx + 4 * (c & 1)), strip_top(mx + 8 + 4 * ((c + 1) & 1)) * sc.dn), sc.dn);
     {
-      const uint32_t kcol = tiles + L::kK + ((n0 >> 6) << 7) + (lane_row(lane, 3, 4, NB) ^ ((n0 & 63) << 1));
-      // column tiles one pair after the other: the part of dO has a factor of its own
+      const uint32_t kcol = tiles + L::kK + block(left_row(lane, NB), n0 >> 4);
+      float Z[kM][kTiles][4] = {};   // the part of dO has a factor of its own
 #pragma unroll
-      for (int i = 0; i < kTiles / 2; ++i) {
-        float Z[kM][2][4] = {};
+      for (int j = 0; j < 4; ++j) {
+        uint32_t wa[kM][4], ya[kM][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int m = 0; m < kM; ++m) {
+          ldsm4(wa[m], block(Wrow, j) + m * 2048);
+          ldsm4(ya[m], block(Urow, j) + m * 2048);
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles / 2; ++i) {
           uint32_t kb[4], qb[4];
           ldsm4t(kb, (kcol ^ (i << 5)) + j * 16 * NB);
           ldsm4t(qb, (kcol ^ (i << 5)) + j * 16 * NB + (L::kQ - L::kK));
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            uint32_t wa[1][4], ya[1][4];
-            ldsm4(wa[0], block(Wrow, j) + m * 2048);
-            ldsm4(ya[0], block(Urow, j) + m * 2048);
-            mul<1>(D[m][2 * i], D[m][2 * i + 1], wa, kb);
-            mul<1>(Z[m][0], Z[m][1], ya, qb);
-          }
+          mul(D, 2 * i, wa, kb);
+          mul(Z, 2 * i, ya, qb);
         }
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            D[m][2 * i][r] = fmaf(co, Z[m][0][r], D[m][2 * i][r]);
-            D[m][2 * i + 1][r] = fmaf(co, Z[m][1][r], D[m][2 * i + 1][r]);
-          }
       }
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) D[m][i][r] = fmaf(co, Z[m][i][r], D[m][i][r]);
     }
     uint32_t rw[kM][4], vw[kM][4];
 #pragma unroll
@@ -819,30 +824,26 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
           vw[m][2 * i + r] = pack_bf16(f0 * (be[i].x * sc.up), f1 * (be[i].y * sc.up));
         }
     const int col = 8 * (lane & 3);
-    const int64_t at = (ht * kChunk + t0w + (lane >> 2)) * s.P + p0 + col;
+    auto at = [&](int i) { return (ht * kChunk + 8 * tile_of(w, i) + (lane >> 2)) * s.P + p0 + col; };
     uint4 out[2];
     // every warp has read dO's tiles by the last barrier: this warp's tokens of the block are its own
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (col < rows)
-        *reinterpret_cast<uint4 *>(o.X16 + at + 8 * i * s.P) =
-            *reinterpret_cast<const uint4 *>(gown + ring + row_at(t0w + 8 * i + (lane >> 2), lane & 3));
-    turned(out, gown + ring, own + ring, rw, t0w, lane);
+        *reinterpret_cast<uint4 *>(o.X16 + at(i)) =
+            *reinterpret_cast<const uint4 *>(gown + ring + row_at(8 * tile_of(w, i) + (lane >> 2), lane & 3));
+    turned(out, gown + ring, own + ring, rw, w, lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (col < rows) *reinterpret_cast<uint4 *>(o.F16 + at + 8 * i * s.P) = out[i];
-    turned(out, gown + ring, own + ring, vw, t0w, lane);
+      if (col < rows) *reinterpret_cast<uint4 *>(o.F16 + at(i)) = out[i];
+    turned(out, gown + ring, own + ring, vw, w, lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tok = t0w + 8 * i + (lane >> 2);
+      const int tok = 8 * tile_of(w, i) + (lane >> 2);
       if (tok < ck.n && col < rows) put_out(dv + (ck.b + tok) * tok_stride + h * s.P + p0 + col, ovec, out[i]);
     }
-    sc.move(D, rescale(strip_top(mx + 4 * (c & 1)), sc.dn));
-    if (c + 1 < nc) {
-      uint32_t x[kM][4];
-      load_x(x, c + 1);
-      take_x(x, c + 1);
-    }
+    sc.move(D, f);
+    if (c + 1 < nc) take_x(c + 1);
   }
   if (live && a.dinit != nullptr) store_state<kTiles>(D, a.dinit + row, sc.up, rows, N, lane);
 }

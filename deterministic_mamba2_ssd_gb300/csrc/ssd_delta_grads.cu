@@ -35,7 +35,7 @@ namespace {
 
 using namespace mma16;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 288;                // eight warps with the products, one that copies
 constexpr int kPMax = 128;
 constexpr int kRow = 2 * kPMax;              // bytes of a token's row of a [token][p] tile in shared memory
 constexpr int kRows = kChunk * kRow;
@@ -43,15 +43,14 @@ constexpr int kRows = kChunk * kRow;
 template <int N>
 struct Smem {
   uint8_t k[kChunk * N * 2], q[kChunk * N * 2];
-  uint8_t X[kRows], F[kRows], E[2][kRows];          // [token][p]; e of this head and the next
+  uint8_t X[2][kRows], F[2][kRows], E[2][kRows];    // [token][p]; of this head and the next
   uint8_t S[kPMax * N * 2], D[kPMax * N * 2];       // [p][n]
   uint8_t m1[kChunk * 128], m2[kChunk * 128];       // [t][s]
-  uint4 kk[2][kThreads], qk[2][kThreads];           // each thread's own part of K K^T and Q K^T, fp16
-  float vec[2][kVec], up[2][8], ub[2][8];           // of this head and the next
+  float vec[2][kVec];                               // of this head and the next
+  uint32_t rel[2][kPMax / 16], even[2];             // the strips' scales relative to the group's, as fp16 pairs
   float fe[2][kChunk];                              // [head parity]: F.e of each token
   float state[2][2][kChunk], down[2][2][kChunk];    // [head parity][column half]: q.Y1 + k.Y2, k.Z
   float wrow[2][2][kChunk], wcol[2][4][kChunk];     // row sums of W by column half, column sums by token strip
-  float inner[2][8];                                // <S0, dS> of each warp's part
 };
 
 __device__ __forceinline__ float quad_sum(float v) {
@@ -68,14 +67,15 @@ __device__ __forceinline__ void scale_a(uint32_t (&a)[4], uint32_t f0, uint32_t 
   }
 }
 
-// d and (kTwo) e, column tiles from n0, += the left operands a and b times 16 rows [k][n] of `tile`.
+// d and (kTwo) e += the left operands a and b times 16 rows [k][n] at `row`; at[i]: this lane's place in them for the
+// i-th 16 columns of its warp.
 template <int kPairs, bool kTwo>
 __device__ __forceinline__ void step_t(float (&d)[2 * kPairs][4], float (&e)[2 * kPairs][4], const uint32_t (&a)[4],
-                                       const uint32_t (&b)[4], uint32_t tile, int n0, int k0, int bytes, int lane) {
+                                       const uint32_t (&b)[4], uint32_t row, const uint32_t (&at)[kPairs]) {
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
     uint32_t r[4];
-    ldsm4t(r, bt_addr(tile, n0 + 16 * i, k0, bytes, lane));
+    ldsm4t(r, row + at[i]);
     mma(d[2 * i], a, r[0], r[1]);
     mma(d[2 * i + 1], a, r[2], r[3]);
     if (kTwo) {
@@ -84,6 +84,8 @@ __device__ __forceinline__ void step_t(float (&d)[2 * kPairs][4], float (&e)[2 *
     }
   }
 }
+// Columns 16 j.. of a row at `row` (tiles are aligned to 128 bytes: the swizzle is an exclusive or of the address).
+__device__ __forceinline__ uint32_t block(uint32_t row, int j) { return (row ^ ((j & 3) << 5)) + ((j >> 2) << 7); }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a, Tiles t, BwdTiles o, int out4) {
@@ -98,43 +100,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   int64_t seq, b, e;
   if (!chunk_of_slot(s, a.cu, slot, seq, b, e)) return;
   const int n = int(e - b);
-  const uint32_t ks = smem_at(sm.k), qs = smem_at(sm.q), Xs = smem_at(sm.X), Fs = smem_at(sm.F),
-                 Ss = smem_at(sm.S), Ds = smem_at(sm.D), m1s = smem_at(sm.m1), m2s = smem_at(sm.m2);
-
-  auto fetch_rows = [&](int i) {   // the [token][p] tiles and the vectors of head i of the group
-    const int h = grp * s.hpg + i;
-    const int64_t ht = slot * s.H + h, at0 = ht * kChunk * P;
-    const uint32_t Es = smem_at(sm.E[i & 1]);
-    const int per = P / 8;   // 16-byte pieces of a row
-    for (int x = tid; x < kChunk * per; x += kThreads) {
-      const int r = x / per, j = x % per;
-      const uint32_t at = swz(r, j, kRow);
-      cp16(Xs + at, o.X16 + at0 + 8 * x);
-      cp16(Fs + at, o.F16 + at0 + 8 * x);
-      cp16(Es + at, t.E16 + at0 + 8 * x);
-    }
-    if (tid < kVec / 4) cp16(smem_at(sm.vec[i & 1]) + 16 * tid, t.vec + ht * kVec + 4 * tid);
-    if (tid < strips) {
-      sm.up[i & 1][tid] = t.up[ht * strips + tid];
-      sm.ub[i & 1][tid] = o.ub[ht * strips + tid];
-    }
-    cp_commit();
-  };
-  auto fetch_state = [&](uint32_t to, const __half *from, int i) {
-    const __half *src = from + (slot * s.H + grp * s.hpg + i) * P * N;
-    for (int x = tid; x < P * N / 8; x += kThreads) cp16(to + 16 * x, src + 8 * x);
-    cp_commit();
-  };
-
-  {
-    const int64_t at = (slot * s.G + grp) * kChunk * N;
-    for (int x = tid; x < kChunk * N / 8; x += kThreads) {
-      cp16(ks + 16 * x, t.K16 + at + 8 * x);
-      cp16(qs + 16 * x, t.Q16 + at + 8 * x);
-    }
-    cp_commit();
-    fetch_rows(0);
-  }
+  const uint32_t ks = smem_at(sm.k), qs = smem_at(sm.q), Ss = smem_at(sm.S), Ds = smem_at(sm.D), m1s = smem_at(sm.m1),
+                 m2s = smem_at(sm.m2);
   // the group's common power of two: the largest of the heads' and strips' up * ub
   float ref = 0.f;
   for (int x = lane; x < s.hpg * strips; x += 32) {
@@ -145,48 +112,134 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   for (int d = 16; d > 0; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(~0u, ref, d));
   const float iref = pow2_inv(ref);
 
-  // dg and dbeta of head i, by one warp, two tokens a lane
-  auto finish = [&](int i) {
-    const int x = i & 1, h = grp * s.hpg + i;
-    const float *vec = sm.vec[x];
-    float inner = 0.f, from[2], cut[2], dn[2];
-#pragma unroll
-    for (int w = 0; w < 8; ++w) inner += sm.inner[x][w];
-    inner *= vec[kVecEg + kChunk - 1];
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int r = 2 * lane + y;
-      from[y] = sm.state[x][0][r] + sm.state[x][1][r];
-      dn[y] = sm.down[x][0][r] + sm.down[x][1][r];
-      cut[y] = (sm.wrow[x][0][r] + sm.wrow[x][1][r]) -
-               ((sm.wcol[x][0][r] + sm.wcol[x][1][r]) + (sm.wcol[x][2][r] + sm.wcol[x][3][r]));
-    }
-    float a1 = from[0] + from[1], a2 = cut[0] + cut[1], a3 = dn[0] + dn[1];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const float u1 = __shfl_down_sync(~0u, a1, d), u2 = __shfl_down_sync(~0u, a2, d), u3 = __shfl_up_sync(~0u, a3, d);
-      if (lane + d < 32) a1 += u1, a2 += u2;
-      if (lane >= d) a3 += u3;
-    }
-    const float b3 = __shfl_up_sync(~0u, a3, 1), n1 = __shfl_down_sync(~0u, a1, 1), n2 = __shfl_down_sync(~0u, a2, 1);
-    const float before = lane == 0 ? 0.f : b3;
-    float dg[2];
-    dg[1] = (lane == 31 ? 0.f : n1 + n2) + from[1] + cut[1] + before + dn[0] + inner;
-    // nothing comes from before the first token but the state
-    dg[0] = a1 + (lane == 0 ? 0.f : a2) + before + inner;
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int r = 2 * lane + y;
-      if (r < n) {
-        static_cast<__nv_bfloat16 *>(a.dg)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * dg[y]);
-        static_cast<__nv_bfloat16 *>(a.dbeta)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * sm.fe[x][r]);
+  if (warp == 8) {
+    auto copy = [&](uint32_t to, const __half *from, int n16) {
+#pragma unroll 8
+      for (int x = lane; x < n16; x += 32) cp16(to + 16 * x, from + 8 * x);
+    };
+    const int per = P / 8, dr = 32 / per, dj = 32 % per;   // 16-byte pieces of a [token][p] row
+    auto fetch_rows = [&](int i) {   // the [token][p] tiles, vectors and scales of head i of the group
+      const int64_t ht = slot * s.H + grp * s.hpg + i, at0 = ht * kChunk * P;
+      const int y = i & 1;
+      const uint32_t Xs = smem_at(sm.X[y]), Fs = smem_at(sm.F[y]), Es = smem_at(sm.E[y]);
+      int r = lane / per, j = lane % per;
+#pragma unroll 4
+      for (int x = lane; x < kChunk * per; x += 32) {
+        const uint32_t at = swz(r, j, kRow);
+        cp16(Xs + at, o.X16 + at0 + 8 * x);
+        cp16(Fs + at, o.F16 + at0 + 8 * x);
+        cp16(Es + at, t.E16 + at0 + 8 * x);
+        r += dr;
+        j += dj;
+        if (j >= per) j -= per, ++r;
       }
+      for (int x = lane; x < kVec / 4; x += 32) cp16(smem_at(sm.vec[y]) + 16 * x, t.vec + ht * kVec + 4 * x);
+      const float f = lane < strips ? t.up[ht * strips + lane] * o.ub[ht * strips + lane] * iref : 1.f;
+      const bool all = __all_sync(~0u, f == 1.f);
+      if (lane < kPMax / 16) sm.rel[y][lane] = twice(f);
+      if (lane == 0) sm.even[y] = all;
+      cp_commit();
+      return f;
+    };
+    // <S0, dS> of head i: the same element of both tiles at the same place; f: the strips' scales, one a lane
+    auto product = [&](float f) {
+      float sum = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < strips; ++j) {
+        float acc = 0.f;
+#pragma unroll 4
+        for (int y = lane; y < 2 * N; y += 32) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(sm.S + 16 * (2 * N * j + y));
+          const uint4 v = *reinterpret_cast<const uint4 *>(sm.D + 16 * (2 * N * j + y));
+          const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float2 fu = unpack(uu[z]), fv = unpack(vv[z]);
+            acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
+          }
+        }
+        sum = fmaf(acc, __shfl_sync(~0u, f, j), sum);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      return sum;
+    };
+    // dg and dbeta of head i, by one warp, two tokens a lane
+    auto finish = [&](int i, float inner) {
+      const int x = i & 1, h = grp * s.hpg + i;
+      const float *vec = sm.vec[x];
+      float from[2], cut[2], dn[2];
+      inner *= vec[kVecEg + kChunk - 1];
+  #pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = 2 * lane + y;
+        from[y] = sm.state[x][0][r] + sm.state[x][1][r];
+        dn[y] = sm.down[x][0][r] + sm.down[x][1][r];
+        cut[y] = (sm.wrow[x][0][r] + sm.wrow[x][1][r]) -
+                 ((sm.wcol[x][0][r] + sm.wcol[x][1][r]) + (sm.wcol[x][2][r] + sm.wcol[x][3][r]));
+      }
+      float a1 = from[0] + from[1], a2 = cut[0] + cut[1], a3 = dn[0] + dn[1];
+  #pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float u1 = __shfl_down_sync(~0u, a1, d), u2 = __shfl_down_sync(~0u, a2, d), u3 = __shfl_up_sync(~0u, a3, d);
+        if (lane + d < 32) a1 += u1, a2 += u2;
+        if (lane >= d) a3 += u3;
+      }
+      const float b3 = __shfl_up_sync(~0u, a3, 1), n1 = __shfl_down_sync(~0u, a1, 1), n2 = __shfl_down_sync(~0u, a2, 1);
+      const float before = lane == 0 ? 0.f : b3;
+      float dg[2];
+      dg[1] = (lane == 31 ? 0.f : n1 + n2) + from[1] + cut[1] + before + dn[0] + inner;
+      // nothing comes from before the first token but the state
+      dg[0] = a1 + (lane == 0 ? 0.f : a2) + before + inner;
+  #pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = 2 * lane + y;
+        if (r < n) {
+          static_cast<__nv_bfloat16 *>(a.dg)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * dg[y]);
+          static_cast<__nv_bfloat16 *>(a.dbeta)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * sm.fe[x][r]);
+        }
+      }
+    };
+    const int64_t at = (slot * s.G + grp) * kChunk * N;
+    copy(ks, t.K16 + at, kChunk * N / 8);
+    copy(qs, t.Q16 + at, kChunk * N / 8);
+    cp_commit();
+    float f = fetch_rows(0), fnext = 1.f, inner = 0.f;
+    cp_wait<1>();
+    __syncthreads();   // k and q
+    for (int i = 0; i < s.hpg; ++i) {
+      cp_wait<0>();
+      __syncthreads();   // rows of head i
+      const int64_t st = (slot * s.H + grp * s.hpg + i) * P * N;
+      copy(Ds, o.D16 + st, P * N / 8);
+      copy(Ss, t.S16 + st, P * N / 8);
+      cp_commit();
+      if (i > 0) finish(i - 1, inner);
+      if (i + 1 < s.hpg) {
+        fnext = fetch_rows(i + 1);
+        cp_wait<1>();
+      } else {
+        cp_wait<0>();
+      }
+      __syncthreads();   // states of head i
+      inner = product(f);
+      f = fnext;
     }
-  };
+    __syncthreads();
+    finish(s.hpg - 1, inner);
+    return;
+  }
 
   const int rows[2] = {16 * wm + g, 16 * wm + g + 8}, n0 = wn * (N / 2);
+  // where this lane's rows of operands begin in their tiles
+  const uint32_t left = ((lane & 7) + (lane & 8)), half = lane >> 4, low = lane & 7;
+  const uint32_t arow = (16 * wm + left) * kRow + ((half ^ low) << 4);            // left operand, X, F, E
+  const uint32_t brow = (32 * wn + low + 8 * half) * kRow + ((((lane >> 3) & 1) ^ low) << 4);   // right operand, E as [n][k]
+  uint32_t at[kPairs];                                                            // right operand, [k][n], this warp's columns
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) at[i] = block(left * NB + ((half ^ low) << 4), wn * kPairs + i);
+  uint32_t kk2[4][2], qk2[4][2];   // this thread's part of K K^T and Q K^T, fp16
   {
-    cp_wait<1>();
     __syncthreads();
     float kk[4][4] = {}, qk[4][4] = {};
 #pragma unroll
@@ -206,12 +259,12 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      sm.kk[i][tid] = make_uint4(pack(kk[2 * i][0], kk[2 * i][1]), pack(kk[2 * i][2], kk[2 * i][3]),
-                                 pack(kk[2 * i + 1][0], kk[2 * i + 1][1]), pack(kk[2 * i + 1][2], kk[2 * i + 1][3]));
-      sm.qk[i][tid] = make_uint4(pack(qk[2 * i][0], qk[2 * i][1]), pack(qk[2 * i][2], qk[2 * i][3]),
-                                 pack(qk[2 * i + 1][0], qk[2 * i + 1][1]), pack(qk[2 * i + 1][2], qk[2 * i + 1][3]));
-    }
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        kk2[y][r] = pack(kk[y][2 * r], kk[y][2 * r + 1]);
+        qk2[y][r] = pack(qk[y][2 * r], qk[y][2 * r + 1]);
+      }
   }
   // this thread's pair of k or q: rows[r], columns n0 + 8 y + c2
   auto pair_of = [&](const uint8_t *tile, int r, int y) {
@@ -233,44 +286,33 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   for (int i = 0; i < s.hpg; ++i) {
     const int x = i & 1;
     const float *vec = sm.vec[x];
-    const uint32_t Es = smem_at(sm.E[x]);
-    cp_wait<0>();
-    __syncthreads();   // this head's rows are here, the head before is done with states and M
-    fetch_state(Ds, o.D16, i);
-    fetch_state(Ss, t.S16, i);
-    if (i > 0 && warp == 0) finish(i - 1);
+    const uint32_t Xs = smem_at(sm.X[x]), Fs = smem_at(sm.F[x]), Es = smem_at(sm.E[x]);
+    __syncthreads();   // this head's rows are here
     const float ka = vec[kVecKa];
-    uint32_t rel[kPMax / 16];   // strips' scales relative to the group's
-    bool even = true;
-#pragma unroll
-    for (int j = 0; j < kPMax / 16; ++j) {
-      const float f = j < strips ? sm.up[x][j] * sm.ub[x][j] * iref : 1.f;
-      rel[j] = twice(f);
-      even &= f == 1.f;
-    }
-    uint32_t aX[kPMax / 16][4], aF[kPMax / 16][4];
+    const bool even = sm.even[x];
     {
+      // blocks above the diagonal go along: a branch would cost more than they do
       float n1[4][4] = {}, n2[4][4] = {};
-#pragma unroll
-      for (int j = 0; j < kPMax / 16; ++j)
-        if (j < strips) {
-          ldsm4(aX[j], a_addr(Xs, 16 * wm, 16 * j, kRow, lane));
-          ldsm4(aF[j], a_addr(Fs, 16 * wm, 16 * j, kRow, lane));
-          if (!even) {
-            scale_a(aX[j], rel[j], rel[j]);
-            scale_a(aF[j], rel[j], rel[j]);
-          }
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            if (2 * wn + y <= wm) {   // blocks up to the diagonal
-              uint32_t bb[4];
-              ldsm4(bb, b_addr(Es, 32 * wn + 16 * y, 16 * j, kRow, lane));
-              mma(n1[2 * y], aF[j], bb[0], bb[1]);
-              mma(n1[2 * y + 1], aF[j], bb[2], bb[3]);
-              mma(n2[2 * y], aX[j], bb[0], bb[1]);
-              mma(n2[2 * y + 1], aX[j], bb[2], bb[3]);
-            }
+#pragma unroll 2
+      for (int j = 0; j < strips; ++j) {
+        uint32_t aX[4], aF[4], bb[2][4];
+        ldsm4(aX, block(Xs + arow, j));
+        ldsm4(aF, block(Fs + arow, j));
+        ldsm4(bb[0], block(Es + brow, j));
+        ldsm4(bb[1], block(Es + brow, j) + 16 * kRow);
+        if (!even) {
+          const uint32_t f = sm.rel[x][j];
+          scale_a(aX, f, f);
+          scale_a(aF, f, f);
         }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          mma(n1[2 * y], aF, bb[y][0], bb[y][1]);
+          mma(n1[2 * y + 1], aF, bb[y][2], bb[y][3]);
+          mma(n2[2 * y], aX, bb[y][0], bb[y][1]);
+          mma(n2[2 * y + 1], aX, bb[y][2], bb[y][3]);
+        }
+      }
       if (wn == wm >> 1 && (lane & 3) == (g >> 1)) {   // this thread has the diagonal's elements g and g + 8
         const int y = 2 * (wm & 1);
         const float(&lo)[4] = y ? n1[2] : n1[0];
@@ -282,71 +324,53 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       const float Lr[2] = {vec[kVecGl + rows[0]], vec[kVecGl + rows[1]]};
       const float w1[2] = {-ka * vec[kVecBeta + rows[0]], -ka * vec[kVecBeta + rows[1]]};
       const float w2 = ka * a.scale;
-      float wrow[2] = {0.f, 0.f};
+      float wrow[2] = {0.f, 0.f}, wcol[8];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int c = 32 * wn + 8 * y + c2;
-        float wcol[2] = {0.f, 0.f};
-        if (2 * wn + (y >> 1) <= wm) {
-          const float2 Gc = *reinterpret_cast<const float2 *>(&vec[kVecG + c]);
-          const float2 Lc = *reinterpret_cast<const float2 *>(&vec[kVecGl + c]);
-          const float2 be = *reinterpret_cast<const float2 *>(&vec[kVecBeta + c]);
-          const uint2 kkw = reinterpret_cast<const uint2 *>(&sm.kk[y >> 1][tid])[y & 1];
-          const uint2 qkw = reinterpret_cast<const uint2 *>(&sm.qk[y >> 1][tid])[y & 1];
+        const float2 Gc = *reinterpret_cast<const float2 *>(&vec[kVecG + c]);
+        const float2 Lc = *reinterpret_cast<const float2 *>(&vec[kVecGl + c]);
+        const float2 be = *reinterpret_cast<const float2 *>(&vec[kVecBeta + c]);
+        wcol[2 * y] = wcol[2 * y + 1] = 0.f;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float d0 = c <= rows[r] ? __expf(acs_diff(Gr[r], Lr[r], Gc.x, Lc.x)) * be.x : 0.f;
-            const float d1 = c + 1 <= rows[r] ? __expf(acs_diff(Gr[r], Lr[r], Gc.y, Lc.y)) * be.y : 0.f;
-            const float x0 = c < rows[r] ? n1[y][2 * r] * d0 * w1[r] : 0.f;
-            const float x1 = c + 1 < rows[r] ? n1[y][2 * r + 1] * d1 * w1[r] : 0.f;
-            const float z0 = c <= rows[r] ? n2[y][2 * r] * d0 * w2 : 0.f;
-            const float z1 = c + 1 <= rows[r] ? n2[y][2 * r + 1] * d1 * w2 : 0.f;
-            const uint32_t at = swz(rows[r], 4 * wn + y, 128) + 2 * c2;
-            *reinterpret_cast<uint32_t *>(sm.m1 + at) = pack(x0, x1);
-            *reinterpret_cast<uint32_t *>(sm.m2 + at) = pack(z0, z1);
-            const float2 kf = unpack(r ? kkw.y : kkw.x), qf = unpack(r ? qkw.y : qkw.x);
-            const float v0 = c < rows[r] ? fmaf(x0, kf.x, z0 * qf.x) : 0.f;
-            const float v1 = c + 1 < rows[r] ? fmaf(x1, kf.y, z1 * qf.y) : 0.f;
-            wrow[r] += v0 + v1;
-            wcol[0] += v0;
-            wcol[1] += v1;
-          }
-        }
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {   // over this strip's 16 tokens
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) wcol[z] += __shfl_xor_sync(~0u, wcol[z], d);
-          if (g == 0) sm.wcol[x][wm][c + z] = wcol[z] * ka;
+        for (int r = 0; r < 2; ++r) {
+          const float d0 = __expf(acs_diff(Gr[r], Lr[r], Gc.x, Lc.x)) * be.x;
+          const float d1 = __expf(acs_diff(Gr[r], Lr[r], Gc.y, Lc.y)) * be.y;
+          const float x0 = c < rows[r] ? n1[y][2 * r] * d0 * w1[r] : 0.f;
+          const float x1 = c + 1 < rows[r] ? n1[y][2 * r + 1] * d1 * w1[r] : 0.f;
+          const float z0 = c <= rows[r] ? n2[y][2 * r] * d0 * w2 : 0.f;
+          const float z1 = c + 1 <= rows[r] ? n2[y][2 * r + 1] * d1 * w2 : 0.f;
+          const uint32_t to = swz(rows[r], 4 * wn + y, 128) + 2 * c2;
+          *reinterpret_cast<uint32_t *>(sm.m1 + to) = pack(x0, x1);
+          *reinterpret_cast<uint32_t *>(sm.m2 + to) = pack(z0, z1);
+          const float2 kf = unpack(kk2[y][r]), qf = unpack(qk2[y][r]);
+          // (the diagonal is not W's: nothing passes from a token to itself)
+          const float v0 = fmaf(x0, kf.x, c < rows[r] ? z0 * qf.x : 0.f);
+          const float v1 = fmaf(x1, kf.y, c + 1 < rows[r] ? z1 * qf.y : 0.f);
+          wrow[r] += v0 + v1;
+          wcol[2 * y] += v0;
+          wcol[2 * y + 1] += v1;
         }
       }
+      // over this strip's 16 tokens: eight columns by eight lanes, halving what each still carries
+#pragma unroll
+      for (int d = 4, lanes = 16; d > 0; d >>= 1, lanes >>= 1) {
+        const bool up = lane & lanes;
+#pragma unroll
+        for (int z = 0; z < d; ++z) {
+          const float give = up ? wcol[z] : wcol[z + d], keep = up ? wcol[z + d] : wcol[z];
+          wcol[z] = keep + __shfl_xor_sync(~0u, give, lanes);
+        }
+      }
+      // left with column 8 y + c2 + z, 2 y + z = g
+      sm.wcol[x][wm][32 * wn + 8 * (g >> 1) + c2 + (g & 1)] = wcol[0] * ka;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         wrow[r] = quad_sum(wrow[r]);
         if (c2 == 0) sm.wrow[x][wn][rows[r]] = wrow[r] * ka;
       }
     }
-    cp_wait<0>();      // the states
-    __syncthreads();   // M1 and M2 are here; X, F, O and v have been read
-    if (i + 1 < s.hpg) fetch_rows(i + 1);
-    {
-      // <S0, dS>: the same element of both tiles at the same place
-      float inner = 0.f;
-      for (int y = tid; y < P * N / 8; y += kThreads) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(sm.S + 16 * y), v = *reinterpret_cast<const uint4 *>(sm.D + 16 * y);
-        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-        const int j = y / (2 * N);   // the strip
-        float acc = 0.f;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const float2 fu = unpack(uu[z]), fv = unpack(vv[z]);
-          acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
-        }
-        inner = fmaf(acc, sm.up[x][j] * sm.ub[x][j] * iref, inner);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) inner += __shfl_xor_sync(~0u, inner, d);
-      if (lane == 0) sm.inner[x][warp] = inner;
-    }
+    __syncthreads();   // M1 and M2 are here, and the states
     uint32_t fx[2], ff[2], fu[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -357,36 +381,37 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     }
     float state[2] = {0.f, 0.f}, down[2] = {0.f, 0.f};
     {
-      float y1[2 * kPairs][4] = {};
-#pragma unroll
-      for (int j = 0; j < kPMax / 16; ++j)
-        if (j < strips) {
-          scale_a(aX[j], fx[0], fx[1]);
-          step_t<kPairs, false>(y1, y1, aX[j], aX[j], Ss, n0, 16 * j, NB, lane);
+      float y1[2 * kPairs][4] = {}, y2[2 * kPairs][4] = {};
+#pragma unroll 2
+      for (int j = 0; j < strips; ++j) {
+        uint32_t aX[4], aF[4];
+        ldsm4(aX, block(Xs + arow, j));
+        ldsm4(aF, block(Fs + arow, j));
+        if (!even) {
+          const uint32_t f = sm.rel[x][j];
+          scale_a(aX, f, f);
+          scale_a(aF, f, f);
         }
+        scale_a(aX, fx[0], fx[1]);
+        scale_a(aF, ff[0], ff[1]);
+        step_t<kPairs, true>(y1, y2, aX, aF, Ss + j * 16 * NB, at);
+      }
       fold(dq, y1, sm.q, state);
-    }
-    {
-      float y2[2 * kPairs][4] = {};
-#pragma unroll
-      for (int j = 0; j < kPMax / 16; ++j)
-        if (j < strips) {
-          scale_a(aF[j], ff[0], ff[1]);
-          step_t<kPairs, false>(y2, y2, aF[j], aF[j], Ss, n0, 16 * j, NB, lane);
-        }
       fold(dk, y2, sm.k, state);
     }
     {
       float z[2 * kPairs][4] = {};
-#pragma unroll
-      for (int j = 0; j < kPMax / 16; ++j)
-        if (j < strips) {
-          uint32_t aE[4];
-          ldsm4(aE, a_addr(Es, 16 * wm, 16 * j, kRow, lane));
-          if (!even) scale_a(aE, rel[j], rel[j]);
-          scale_a(aE, fu[0], fu[1]);
-          step_t<kPairs, false>(z, z, aE, aE, Ds, n0, 16 * j, NB, lane);
+#pragma unroll 2
+      for (int j = 0; j < strips; ++j) {
+        uint32_t aE[4];
+        ldsm4(aE, block(Es + arow, j));
+        if (!even) {
+          const uint32_t f = sm.rel[x][j];
+          scale_a(aE, f, f);
         }
+        scale_a(aE, fu[0], fu[1]);
+        step_t<kPairs, false>(z, z, aE, aE, Ds + j * 16 * NB, at);
+      }
       fold(dk, z, sm.k, down);
     }
 #pragma unroll
@@ -404,36 +429,35 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       uint32_t a2[4], a1[4];
       ldsm4(a2, a_addr(m2s, 16 * wm, 16 * j, 128, lane));
       ldsm4(a1, a_addr(m1s, 16 * wm, 16 * j, 128, lane));
-      step_t<kPairs, true>(dq, dk, a2, a1, ks, n0, 16 * j, NB, lane);
+      step_t<kPairs, true>(dq, dk, a2, a1, ks + j * 16 * NB, at);
     }
 #pragma unroll 1
     for (int j = wm; j < 4; ++j) {
       uint32_t a1[4], a2[4];
       ldsm4t(a1, at_addr(m1s, 16 * wm, 16 * j, 128, lane));
       ldsm4t(a2, at_addr(m2s, 16 * wm, 16 * j, 128, lane));
-      step_t<kPairs, false>(dk, dk, a1, a1, ks, n0, 16 * j, NB, lane);
-      step_t<kPairs, false>(dk, dk, a2, a2, qs, n0, 16 * j, NB, lane);
+      step_t<kPairs, false>(dk, dk, a1, a1, ks + j * 16 * NB, at);
+      step_t<kPairs, false>(dk, dk, a2, a2, qs + j * 16 * NB, at);
     }
   }
-  __syncthreads();
-  if (warp == 0) finish(s.hpg - 1);
+  __syncthreads();   // what the copying warp still has to finish
   __nv_bfloat16 *oq = static_cast<__nv_bfloat16 *>(a.dq), *ok = static_cast<__nv_bfloat16 *>(a.dk);
 #pragma unroll
   for (int r = 0; r < 2; ++r)
     if (rows[r] < n) {
-      const int64_t at = ((b + rows[r]) * s.G + grp) * N + n0 + c2;
+      const int64_t to = ((b + rows[r]) * s.G + grp) * N + n0 + c2;
 #pragma unroll
       for (int y = 0; y < 2 * kPairs; ++y) {
         const uint32_t vq = pack_bf16(dq[y][2 * r] * ref, dq[y][2 * r + 1] * ref);
         const uint32_t vk = pack_bf16(dk[y][2 * r] * ref, dk[y][2 * r + 1] * ref);
         if (out4) {
-          *reinterpret_cast<uint32_t *>(oq + at + 8 * y) = vq;
-          *reinterpret_cast<uint32_t *>(ok + at + 8 * y) = vk;
+          *reinterpret_cast<uint32_t *>(oq + to + 8 * y) = vq;
+          *reinterpret_cast<uint32_t *>(ok + to + 8 * y) = vk;
         } else {
-          oq[at + 8 * y] = __ushort_as_bfloat16(static_cast<unsigned short>(vq & 0xffffu));
-          oq[at + 8 * y + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(vq >> 16));
-          ok[at + 8 * y] = __ushort_as_bfloat16(static_cast<unsigned short>(vk & 0xffffu));
-          ok[at + 8 * y + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(vk >> 16));
+          oq[to + 8 * y] = __ushort_as_bfloat16(static_cast<unsigned short>(vq & 0xffffu));
+          oq[to + 8 * y + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(vq >> 16));
+          ok[to + 8 * y] = __ushort_as_bfloat16(static_cast<unsigned short>(vk & 0xffffu));
+          ok[to + 8 * y + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(vk >> 16));
         }
       }
     }

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
       const float Gr[2] = {G[rows[0]], G[rows[1]]}, Glr[2] = {Gl[rows[0]], Gl[rows[1]]};
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j <= 2 * warp + 1) {   // blocks above the diagonal are never read
+        if (j <= 2 * (warp | 1) + 1) {   // of the blocks above the diagonal, two are read
           const int c = 8 * j + 2 * (lane & 3);
           const float g0 = G[c], g1 = G[c + 1], l0 = Gl[c], l1 = Gl[c + 1];
 #pragma unroll

@@ -10,7 +10,8 @@
 //   Y16 (slot, head):        (I + L diag(beta))^-1 L, rows [t][s] times
 //                            2^-tau_t; a second plane with the rounding left over
 //   P16 (slot, head):        exp(G_t - G_s) (q16_t . k16_s), s <= t
-//                            (16 x 16 blocks above the diagonal not written)
+//                            (zero above the diagonal; there, only the 16 x 16
+//                            blocks (0, 1) and (2, 3) are written)
 //   vec (slot, head):        kVec floats, see the offsets below
 //   S16 (slot, head):        state entering the chunk, rows [p][n] times 2^-r
 //   E16 (slot, head):        e of the chunk, rows [t][p] (not swizzled) times 2^-r
