@@ -35,7 +35,8 @@ namespace {
 
 using namespace mma16;
 
-constexpr int kThreads = 288;                // eight warps with the products, one that copies
+constexpr int kWork = 256, kCopy = 128;      // threads with the products, threads that copy
+constexpr int kThreads = kWork + kCopy;
 constexpr int kPMax = 128;
 constexpr int kRow = 2 * kPMax;              // bytes of a token's row of a [token][p] tile in shared memory
 constexpr int kRows = kChunk * kRow;
@@ -47,7 +48,9 @@ struct Smem {
   uint8_t S[kPMax * N * 2], D[kPMax * N * 2];       // [p][n]
   uint8_t m1[kChunk * 128], m2[kChunk * 128];       // [t][s]
   float vec[2][kVec];                               // of this head and the next
-  uint32_t rel[2][kPMax / 16], even[2];             // the strips' scales relative to the group's, as fp16 pairs
+  float rel[2][kPMax / 16];                         // the strips' scales relative to the group's
+  uint32_t even[2];                                 // all of them 1
+  float inner[2][kCopy / 32];                       // <S0, dS>, each copying warp's part
   float fe[2][kChunk];                              // [head parity]: F.e of each token
   float state[2][2][kChunk], down[2][2][kChunk];    // [head parity][column half]: q.Y1 + k.Y2, k.Z
   float wrow[2][2][kChunk], wcol[2][4][kChunk];     // row sums of W by column half, column sums by token strip
@@ -112,19 +115,20 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   for (int d = 16; d > 0; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(~0u, ref, d));
   const float iref = pow2_inv(ref);
 
-  if (warp == 8) {
+  if (tid >= kWork) {
+    const int ct = tid - kWork;
     auto copy = [&](uint32_t to, const __half *from, int n16) {
 #pragma unroll 8
-      for (int x = lane; x < n16; x += 32) cp16(to + 16 * x, from + 8 * x);
+      for (int x = ct; x < n16; x += kCopy) cp16(to + 16 * x, from + 8 * x);
     };
-    const int per = P / 8, dr = 32 / per, dj = 32 % per;   // 16-byte pieces of a [token][p] row
+    const int per = P / 8, dr = kCopy / per, dj = kCopy % per;   // 16-byte pieces of a [token][p] row
     auto fetch_rows = [&](int i) {   // the [token][p] tiles, vectors and scales of head i of the group
       const int64_t ht = slot * s.H + grp * s.hpg + i, at0 = ht * kChunk * P;
       const int y = i & 1;
       const uint32_t Xs = smem_at(sm.X[y]), Fs = smem_at(sm.F[y]), Es = smem_at(sm.E[y]);
-      int r = lane / per, j = lane % per;
+      int r = ct / per, j = ct % per;
 #pragma unroll 4
-      for (int x = lane; x < kChunk * per; x += 32) {
+      for (int x = ct; x < kChunk * per; x += kCopy) {
         const uint32_t at = swz(r, j, kRow);
         cp16(Xs + at, o.X16 + at0 + 8 * x);
         cp16(Fs + at, o.F16 + at0 + 8 * x);
@@ -133,24 +137,24 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
         j += dj;
         if (j >= per) j -= per, ++r;
       }
-      for (int x = lane; x < kVec / 4; x += 32) cp16(smem_at(sm.vec[y]) + 16 * x, t.vec + ht * kVec + 4 * x);
-      const float f = lane < strips ? t.up[ht * strips + lane] * o.ub[ht * strips + lane] * iref : 1.f;
-      const bool all = __all_sync(~0u, f == 1.f);
-      if (lane < kPMax / 16) sm.rel[y][lane] = twice(f);
-      if (lane == 0) sm.even[y] = all;
+      if (warp == 8) {   // which has read the vectors of two heads before
+        for (int x = lane; x < kVec / 4; x += 32) cp16(smem_at(sm.vec[y]) + 16 * x, t.vec + ht * kVec + 4 * x);
+        const float f = lane < strips ? t.up[ht * strips + lane] * o.ub[ht * strips + lane] * iref : 1.f;
+        const bool all = __all_sync(~0u, f == 1.f);
+        if (lane < kPMax / 16) sm.rel[y][lane] = f;
+        if (lane == 0) sm.even[y] = all;
+      }
       cp_commit();
-      return f;
     };
-    // <S0, dS> of head i: the same element of both tiles at the same place; f: the strips' scales, one a lane
-    auto product = [&](float f) {
+    auto product = [&](int i) {   // the same element of both states at the same place
       float sum = 0.f;
 #pragma unroll 1
       for (int j = 0; j < strips; ++j) {
         float acc = 0.f;
-#pragma unroll 4
-        for (int y = lane; y < 2 * N; y += 32) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(sm.S + 16 * (2 * N * j + y));
-          const uint4 v = *reinterpret_cast<const uint4 *>(sm.D + 16 * (2 * N * j + y));
+#pragma unroll
+        for (int y = 0; y < 2 * N; y += kCopy) {
+          const int at = 16 * (2 * N * j + y + ct);
+          const uint4 u = *reinterpret_cast<const uint4 *>(sm.S + at), v = *reinterpret_cast<const uint4 *>(sm.D + at);
           const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
@@ -158,18 +162,18 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
             acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
           }
         }
-        sum = fmaf(acc, __shfl_sync(~0u, f, j), sum);
+        sum = fmaf(acc, sm.rel[i & 1][j], sum);
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-      return sum;
+      if (lane == 0) sm.inner[i & 1][ct >> 5] = sum;
     };
     // dg and dbeta of head i, by one warp, two tokens a lane
-    auto finish = [&](int i, float inner) {
+    auto finish = [&](int i) {
       const int x = i & 1, h = grp * s.hpg + i;
       const float *vec = sm.vec[x];
       float from[2], cut[2], dn[2];
-      inner *= vec[kVecEg + kChunk - 1];
+      const float inner = (sm.inner[x][0] + sm.inner[x][1] + sm.inner[x][2] + sm.inner[x][3]) * vec[kVecEg + kChunk - 1];
   #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = 2 * lane + y;
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     copy(ks, t.K16 + at, kChunk * N / 8);
     copy(qs, t.Q16 + at, kChunk * N / 8);
     cp_commit();
-    float f = fetch_rows(0), fnext = 1.f, inner = 0.f;
+    fetch_rows(0);
     cp_wait<1>();
     __syncthreads();   // k and q
     for (int i = 0; i < s.hpg; ++i) {
@@ -214,19 +218,18 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       copy(Ds, o.D16 + st, P * N / 8);
       copy(Ss, t.S16 + st, P * N / 8);
       cp_commit();
-      if (i > 0) finish(i - 1, inner);
+      if (i > 0 && warp == 8) finish(i - 1);
       if (i + 1 < s.hpg) {
-        fnext = fetch_rows(i + 1);
+        fetch_rows(i + 1);
         cp_wait<1>();
       } else {
         cp_wait<0>();
       }
       __syncthreads();   // states of head i
-      inner = product(f);
-      f = fnext;
+      product(i);
     }
     __syncthreads();
-    finish(s.hpg - 1, inner);
+    if (warp == 8) finish(s.hpg - 1);
     return;
   }
 
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
         ldsm4(bb[0], block(Es + brow, j));
         ldsm4(bb[1], block(Es + brow, j) + 16 * kRow);
         if (!even) {
-          const uint32_t f = sm.rel[x][j];
+          const uint32_t f = twice(sm.rel[x][j]);
           scale_a(aX, f, f);
           scale_a(aF, f, f);
         }
@@ -313,36 +316,34 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
           mma(n2[2 * y + 1], aX, bb[y][2], bb[y][3]);
         }
       }
-      if (wn == wm >> 1 && (lane & 3) == (g >> 1)) {   // this thread has the diagonal's elements g and g + 8
-        const int y = 2 * (wm & 1);
-        const float(&lo)[4] = y ? n1[2] : n1[0];
-        const float(&hi)[4] = y ? n1[3] : n1[1];
-        sm.fe[x][rows[0]] = g & 1 ? lo[1] : lo[0];
-        sm.fe[x][rows[1]] = g & 1 ? hi[3] : hi[2];
-      }
       const float Gr[2] = {vec[kVecG + rows[0]], vec[kVecG + rows[1]]};
       const float Lr[2] = {vec[kVecGl + rows[0]], vec[kVecGl + rows[1]]};
       const float w1[2] = {-ka * vec[kVecBeta + rows[0]], -ka * vec[kVecBeta + rows[1]]};
       const float w2 = ka * a.scale;
       float wrow[2] = {0.f, 0.f}, wcol[8];
+      float2 Gc[4], Lc[4], be[4];   // all of them first: the stores below would hold back the loads after them
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int c = 32 * wn + 8 * y + c2;
-        const float2 Gc = *reinterpret_cast<const float2 *>(&vec[kVecG + c]);
-        const float2 Lc = *reinterpret_cast<const float2 *>(&vec[kVecGl + c]);
-        const float2 be = *reinterpret_cast<const float2 *>(&vec[kVecBeta + c]);
+        Gc[y] = *reinterpret_cast<const float2 *>(&vec[kVecG + c]);
+        Lc[y] = *reinterpret_cast<const float2 *>(&vec[kVecGl + c]);
+        be[y] = *reinterpret_cast<const float2 *>(&vec[kVecBeta + c]);
+      }
+      uint32_t m1[4][2], m2[4][2];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int c = 32 * wn + 8 * y + c2;
         wcol[2 * y] = wcol[2 * y + 1] = 0.f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float d0 = __expf(acs_diff(Gr[r], Lr[r], Gc.x, Lc.x)) * be.x;
-          const float d1 = __expf(acs_diff(Gr[r], Lr[r], Gc.y, Lc.y)) * be.y;
+          const float d0 = __expf(acs_diff(Gr[r], Lr[r], Gc[y].x, Lc[y].x)) * be[y].x;
+          const float d1 = __expf(acs_diff(Gr[r], Lr[r], Gc[y].y, Lc[y].y)) * be[y].y;
           const float x0 = c < rows[r] ? n1[y][2 * r] * d0 * w1[r] : 0.f;
           const float x1 = c + 1 < rows[r] ? n1[y][2 * r + 1] * d1 * w1[r] : 0.f;
           const float z0 = c <= rows[r] ? n2[y][2 * r] * d0 * w2 : 0.f;
           const float z1 = c + 1 <= rows[r] ? n2[y][2 * r + 1] * d1 * w2 : 0.f;
-          const uint32_t to = swz(rows[r], 4 * wn + y, 128) + 2 * c2;
-          *reinterpret_cast<uint32_t *>(sm.m1 + to) = pack(x0, x1);
-          *reinterpret_cast<uint32_t *>(sm.m2 + to) = pack(z0, z1);
+          m1[y][r] = pack(x0, x1);
+          m2[y][r] = pack(z0, z1);
           const float2 kf = unpack(kk2[y][r]), qf = unpack(qk2[y][r]);
           // (the diagonal is not W's: nothing passes from a token to itself)
           const float v0 = fmaf(x0, kf.x, c < rows[r] ? z0 * qf.x : 0.f);
@@ -352,6 +353,21 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
           wcol[2 * y + 1] += v1;
         }
       }
+      if (wn == wm >> 1 && (lane & 3) == (g >> 1)) {   // this thread has the diagonal's elements g and g + 8
+        const int y = 2 * (wm & 1);
+        const float(&lo)[4] = y ? n1[2] : n1[0];
+        const float(&hi)[4] = y ? n1[3] : n1[1];
+        sm.fe[x][rows[0]] = g & 1 ? lo[1] : lo[0];
+        sm.fe[x][rows[1]] = g & 1 ? hi[3] : hi[2];
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t to = swz(rows[r], 4 * wn + y, 128) + 2 * c2;
+          *reinterpret_cast<uint32_t *>(sm.m1 + to) = m1[y][r];
+          *reinterpret_cast<uint32_t *>(sm.m2 + to) = m2[y][r];
+        }
       // over this strip's 16 tokens: eight columns by eight lanes, halving what each still carries
 #pragma unroll
       for (int d = 4, lanes = 16; d > 0; d >>= 1, lanes >>= 1) {
@@ -382,13 +398,23 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     float state[2] = {0.f, 0.f}, down[2] = {0.f, 0.f};
     {
       float y1[2 * kPairs][4] = {}, y2[2 * kPairs][4] = {};
+      uint32_t nX[4], nF[4];   // the left operands a step ahead
+      ldsm4(nX, Xs + arow);
+      ldsm4(nF, Fs + arow);
 #pragma unroll 2
       for (int j = 0; j < strips; ++j) {
         uint32_t aX[4], aF[4];
-        ldsm4(aX, block(Xs + arow, j));
-        ldsm4(aF, block(Fs + arow, j));
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          aX[z] = nX[z];
+          aF[z] = nF[z];
+        }
+        if (j + 1 < strips) {
+          ldsm4(nX, block(Xs + arow, j + 1));
+          ldsm4(nF, block(Fs + arow, j + 1));
+        }
         if (!even) {
-          const uint32_t f = sm.rel[x][j];
+          const uint32_t f = twice(sm.rel[x][j]);
           scale_a(aX, f, f);
           scale_a(aF, f, f);
         }
@@ -401,12 +427,16 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     }
     {
       float z[2 * kPairs][4] = {};
+      uint32_t nE[4];
+      ldsm4(nE, Es + arow);
 #pragma unroll 2
       for (int j = 0; j < strips; ++j) {
         uint32_t aE[4];
-        ldsm4(aE, block(Es + arow, j));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) aE[y] = nE[y];
+        if (j + 1 < strips) ldsm4(nE, block(Es + arow, j + 1));
         if (!even) {
-          const uint32_t f = sm.rel[x][j];
+          const uint32_t f = twice(sm.rel[x][j]);
           scale_a(aE, f, f);
         }
         scale_a(aE, fu[0], fu[1]);
