@@ -35,8 +35,7 @@ namespace {
 
 using namespace mma16;
 
-constexpr int kWork = 256, kCopy = 128;      // threads with the products, threads that copy
-constexpr int kThreads = kWork + kCopy;
+constexpr int kThreads = 512;
 constexpr int kPMax = 128;
 constexpr int kRow = 2 * kPMax;              // bytes of a token's row of a [token][p] tile in shared memory
 constexpr int kRows = kChunk * kRow;
@@ -47,13 +46,13 @@ struct Smem {
   uint8_t X[2][kRows], F[2][kRows], E[2][kRows];    // [token][p]; of this head and the next
   uint8_t S[kPMax * N * 2], D[kPMax * N * 2];       // [p][n]
   uint8_t m1[kChunk * 128], m2[kChunk * 128];       // [t][s]
-  float vec[2][kVec];                               // of this head and the next
+  float vec[3][kVec];                               // of the head before, this one and the next
   float rel[2][kPMax / 16];                         // the strips' scales relative to the group's
   uint32_t even[2];                                 // all of them 1
-  float inner[2][kCopy / 32];                       // <S0, dS>, each copying warp's part
+  float inner[2][kThreads / 32];                    // <S0, dS>, each warp's part
   float fe[2][kChunk];                              // [head parity]: F.e of each token
-  float state[2][2][kChunk], down[2][2][kChunk];    // [head parity][column half]: q.Y1 + k.Y2, k.Z
-  float wrow[2][2][kChunk], wcol[2][4][kChunk];     // row sums of W by column half, column sums by token strip
+  float state[2][4][kChunk], down[2][4][kChunk];    // [head parity][column quarter]: q.Y1 + k.Y2, k.Z
+  float wrow[2][4][kChunk], wcol[2][4][kChunk];     // row sums of W by column quarter, column sums by token strip
 };
 
 __device__ __forceinline__ float quad_sum(float v) {
@@ -93,10 +92,12 @@ __device__ __forceinline__ uint32_t block(uint32_t row, int j) { return (row ^ (
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a, Tiles t, BwdTiles o, int out4) {
   constexpr int NB = 2 * N;          // bytes of a row of k, q, S, D
-  constexpr int kPairs = N / 32;     // pairs of column tiles of a warp (half of the columns)
+  constexpr int kPairs = N / 64;     // pairs of column tiles of a warp (a quarter of the columns)
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<N> &sm = *reinterpret_cast<Smem<N> *>(raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wm = warp & 3, wn = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wn = warp >> 2;
+  // the strip of tokens: of the ten 16 x 16 blocks that the triangle has, each scheduler gets two or three
+  const int wm = ((wn < 2 ? 0x3210 : wn == 2 ? 0x3102 : 0x2103) >> (4 * (warp & 3))) & 3;
   const int64_t slot = blockIdx.x;
   const int grp = blockIdx.y, g = lane >> 2, c2 = 2 * (lane & 3);
   const int P = s.P, strips = P / 16;
@@ -115,159 +116,112 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   for (int d = 16; d > 0; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(~0u, ref, d));
   const float iref = pow2_inv(ref);
 
-  if (tid >= kWork) {
-    const int ct = tid - kWork;
-    auto copy = [&](uint32_t to, const __half *from, int n16) {
-#pragma unroll 8
-      for (int x = ct; x < n16; x += kCopy) cp16(to + 16 * x, from + 8 * x);
-    };
-    const int per = P / 8, dr = kCopy / per, dj = kCopy % per;   // 16-byte pieces of a [token][p] row
-    auto fetch_rows = [&](int i) {   // the [token][p] tiles, vectors and scales of head i of the group
-      const int64_t ht = slot * s.H + grp * s.hpg + i, at0 = ht * kChunk * P;
-      const int y = i & 1;
-      const uint32_t Xs = smem_at(sm.X[y]), Fs = smem_at(sm.F[y]), Es = smem_at(sm.E[y]);
-      int r = ct / per, j = ct % per;
-#pragma unroll 4
-      for (int x = ct; x < kChunk * per; x += kCopy) {
-        const uint32_t at = swz(r, j, kRow);
-        cp16(Xs + at, o.X16 + at0 + 8 * x);
-        cp16(Fs + at, o.F16 + at0 + 8 * x);
-        cp16(Es + at, t.E16 + at0 + 8 * x);
-        r += dr;
-        j += dj;
-        if (j >= per) j -= per, ++r;
-      }
-      if (warp == 8) {   // which has read the vectors of two heads before
-        for (int x = lane; x < kVec / 4; x += 32) cp16(smem_at(sm.vec[y]) + 16 * x, t.vec + ht * kVec + 4 * x);
-        const float f = lane < strips ? t.up[ht * strips + lane] * o.ub[ht * strips + lane] * iref : 1.f;
-        const bool all = __all_sync(~0u, f == 1.f);
-        if (lane < kPMax / 16) sm.rel[y][lane] = f;
-        if (lane == 0) sm.even[y] = all;
-      }
-      cp_commit();
-    };
-    auto product = [&](int i) {   // the same element of both states at the same place
-      float sum = 0.f;
-#pragma unroll 1
-      for (int j = 0; j < strips; ++j) {
-        float acc = 0.f;
-#pragma unroll
-        for (int y = 0; y < 2 * N; y += kCopy) {
-          const int at = 16 * (2 * N * j + y + ct);
-          const uint4 u = *reinterpret_cast<const uint4 *>(sm.S + at), v = *reinterpret_cast<const uint4 *>(sm.D + at);
-          const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const float2 fu = unpack(uu[z]), fv = unpack(vv[z]);
-            acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
-          }
-        }
-        sum = fmaf(acc, sm.rel[i & 1][j], sum);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-      if (lane == 0) sm.inner[i & 1][ct >> 5] = sum;
-    };
-    // dg and dbeta of head i, by one warp, two tokens a lane
-    auto finish = [&](int i) {
-      const int x = i & 1, h = grp * s.hpg + i;
-      const float *vec = sm.vec[x];
-      float from[2], cut[2], dn[2];
-      const float inner = (sm.inner[x][0] + sm.inner[x][1] + sm.inner[x][2] + sm.inner[x][3]) * vec[kVecEg + kChunk - 1];
-  #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int r = 2 * lane + y;
-        from[y] = sm.state[x][0][r] + sm.state[x][1][r];
-        dn[y] = sm.down[x][0][r] + sm.down[x][1][r];
-        cut[y] = (sm.wrow[x][0][r] + sm.wrow[x][1][r]) -
-                 ((sm.wcol[x][0][r] + sm.wcol[x][1][r]) + (sm.wcol[x][2][r] + sm.wcol[x][3][r]));
-      }
-      float a1 = from[0] + from[1], a2 = cut[0] + cut[1], a3 = dn[0] + dn[1];
-  #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const float u1 = __shfl_down_sync(~0u, a1, d), u2 = __shfl_down_sync(~0u, a2, d), u3 = __shfl_up_sync(~0u, a3, d);
-        if (lane + d < 32) a1 += u1, a2 += u2;
-        if (lane >= d) a3 += u3;
-      }
-      const float b3 = __shfl_up_sync(~0u, a3, 1), n1 = __shfl_down_sync(~0u, a1, 1), n2 = __shfl_down_sync(~0u, a2, 1);
-      const float before = lane == 0 ? 0.f : b3;
-      float dg[2];
-      dg[1] = (lane == 31 ? 0.f : n1 + n2) + from[1] + cut[1] + before + dn[0] + inner;
-      // nothing comes from before the first token but the state
-      dg[0] = a1 + (lane == 0 ? 0.f : a2) + before + inner;
-  #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int r = 2 * lane + y;
-        if (r < n) {
-          static_cast<__nv_bfloat16 *>(a.dg)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * dg[y]);
-          static_cast<__nv_bfloat16 *>(a.dbeta)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * sm.fe[x][r]);
-        }
-      }
-    };
-    const int64_t at = (slot * s.G + grp) * kChunk * N;
-    copy(ks, t.K16 + at, kChunk * N / 8);
-    copy(qs, t.Q16 + at, kChunk * N / 8);
-    cp_commit();
-    fetch_rows(0);
-    cp_wait<1>();
-    __syncthreads();   // k and q
-    for (int i = 0; i < s.hpg; ++i) {
-      cp_wait<0>();
-      __syncthreads();   // rows of head i
-      const int64_t st = (slot * s.H + grp * s.hpg + i) * P * N;
-      copy(Ds, o.D16 + st, P * N / 8);
-      copy(Ss, t.S16 + st, P * N / 8);
-      cp_commit();
-      if (i > 0 && warp == 8) finish(i - 1);
-      if (i + 1 < s.hpg) {
-        fetch_rows(i + 1);
-        cp_wait<1>();
-      } else {
-        cp_wait<0>();
-      }
-      __syncthreads();   // states of head i
-      product(i);
+  auto copy = [&](uint32_t to, const __half *from, int n16) {
+    for (int x = tid; x < n16; x += kThreads) cp16(to + 16 * x, from + 8 * x);
+  };
+  const int per = P / 8, r0 = tid / per, j0 = tid % per, dr = kThreads / per, dj = kThreads % per;
+  auto fetch_rows = [&](int i) {   // the [token][p] tiles (16-byte pieces, `per` of a row), vectors, scales of head i of the group
+    const int64_t ht = slot * s.H + grp * s.hpg + i, at0 = ht * kChunk * P;
+    const int y = i & 1;
+    const uint32_t Xs = smem_at(sm.X[y]), Fs = smem_at(sm.F[y]), Es = smem_at(sm.E[y]);
+    int r = r0, j = j0;
+    for (int x = tid; x < kChunk * per; x += kThreads) {
+      const uint32_t at = swz(r, j, kRow);
+      cp16(Xs + at, o.X16 + at0 + 8 * x);
+      cp16(Fs + at, o.F16 + at0 + 8 * x);
+      cp16(Es + at, t.E16 + at0 + 8 * x);
+      r += dr;
+      j += dj;
+      if (j >= per) j -= per, ++r;
     }
-    __syncthreads();
-    if (warp == 8) finish(s.hpg - 1);
-    return;
-  }
+    if (tid < kVec / 4) cp16(smem_at(sm.vec[i % 3]) + 16 * tid, t.vec + ht * kVec + 4 * tid);
+    if (warp == kThreads / 32 - 1) {
+      const float f = lane < strips ? t.up[ht * strips + lane] * o.ub[ht * strips + lane] * iref : 1.f;
+      const bool all = __all_sync(~0u, f == 1.f);
+      if (lane < kPMax / 16) sm.rel[y][lane] = f;
+      if (lane == 0) sm.even[y] = all;
+    }
+    cp_commit();
+  };
 
-  const int rows[2] = {16 * wm + g, 16 * wm + g + 8}, n0 = wn * (N / 2);
+  // dg and dbeta of head i, by one warp, two tokens a lane
+  auto finish = [&](int i) {
+    const int x = i & 1, h = grp * s.hpg + i;
+    float from[2], cut[2], dn[2], inner = lane < kThreads / 32 ? sm.inner[x][lane] : 0.f;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) inner += __shfl_xor_sync(~0u, inner, d);
+    inner = __shfl_sync(~0u, inner, 0) * sm.vec[i % 3][kVecEg + kChunk - 1];
+    auto four = [](const float (&v)[4][kChunk], int r) { return (v[0][r] + v[1][r]) + (v[2][r] + v[3][r]); };
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int r = 2 * lane + y;
+      from[y] = four(sm.state[x], r);
+      dn[y] = four(sm.down[x], r);
+      cut[y] = four(sm.wrow[x], r) - four(sm.wcol[x], r);
+    }
+    float a1 = from[0] + from[1], a2 = cut[0] + cut[1], a3 = dn[0] + dn[1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float u1 = __shfl_down_sync(~0u, a1, d), u2 = __shfl_down_sync(~0u, a2, d), u3 = __shfl_up_sync(~0u, a3, d);
+      if (lane + d < 32) a1 += u1, a2 += u2;
+      if (lane >= d) a3 += u3;
+    }
+    const float b3 = __shfl_up_sync(~0u, a3, 1), n1 = __shfl_down_sync(~0u, a1, 1), n2 = __shfl_down_sync(~0u, a2, 1);
+    const float before = lane == 0 ? 0.f : b3;
+    float dg[2];
+    dg[1] = (lane == 31 ? 0.f : n1 + n2) + from[1] + cut[1] + before + dn[0] + inner;
+    // nothing comes from before the first token but the state
+    dg[0] = a1 + (lane == 0 ? 0.f : a2) + before + inner;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int r = 2 * lane + y;
+      if (r < n) {
+        static_cast<__nv_bfloat16 *>(a.dg)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * dg[y]);
+        static_cast<__nv_bfloat16 *>(a.dbeta)[(b + r) * s.H + h] = __float2bfloat16_rn(ref * sm.fe[x][r]);
+      }
+    }
+  };
+
+  const int rows[2] = {16 * wm + g, 16 * wm + g + 8}, n0 = wn * (N / 4);
   // where this lane's rows of operands begin in their tiles
-  const uint32_t left = ((lane & 7) + (lane & 8)), half = lane >> 4, low = lane & 7;
+  const uint32_t left = (lane & 7) + (lane & 8), half = lane >> 4, low = lane & 7;
   const uint32_t arow = (16 * wm + left) * kRow + ((half ^ low) << 4);            // left operand, X, F, E
-  const uint32_t brow = (32 * wn + low + 8 * half) * kRow + ((((lane >> 3) & 1) ^ low) << 4);   // right operand, E as [n][k]
+  const uint32_t brow = (16 * wn + low + 8 * half) * kRow + ((((lane >> 3) & 1) ^ low) << 4);   // right operand, E as [n][k]
   uint32_t at[kPairs];                                                            // right operand, [k][n], this warp's columns
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) at[i] = block(left * NB + ((half ^ low) << 4), wn * kPairs + i);
-  uint32_t kk2[4][2], qk2[4][2];   // this thread's part of K K^T and Q K^T, fp16
+  uint32_t kk2[2][2] = {}, qk2[2][2] = {};   // this thread's part of K K^T and Q K^T, fp16: block (wm, wn)
   {
+    const int64_t from = (slot * s.G + grp) * kChunk * N;
+    copy(ks, t.K16 + from, kChunk * N / 8);
+    copy(qs, t.Q16 + from, kChunk * N / 8);
+    cp_commit();
+    fetch_rows(0);
+    // blocks above the diagonal have no sums
+    for (int x = tid; x < 8 * kChunk; x += kThreads) (&sm.wrow[0][0][0])[x] = (&sm.wcol[0][0][0])[x] = 0.f;
+    cp_wait<1>();
     __syncthreads();
-    float kk[4][4] = {}, qk[4][4] = {};
+    if (wn <= wm) {
+      float kk[2][4] = {}, qk[2][4] = {};
 #pragma unroll
-    for (int k0 = 0; k0 < N; k0 += 16) {
-      uint32_t ak[4], aq[4];
-      ldsm4(ak, a_addr(ks, 16 * wm, k0, NB, lane));
-      ldsm4(aq, a_addr(qs, 16 * wm, k0, NB, lane));
+      for (int k0 = 0; k0 < N; k0 += 16) {
+        uint32_t ak[4], aq[4], bb[4];
+        ldsm4(ak, a_addr(ks, 16 * wm, k0, NB, lane));
+        ldsm4(aq, a_addr(qs, 16 * wm, k0, NB, lane));
+        ldsm4(bb, b_addr(ks, 16 * wn, k0, NB, lane));
+        mma(kk[0], ak, bb[0], bb[1]);
+        mma(kk[1], ak, bb[2], bb[3]);
+        mma(qk[0], aq, bb[0], bb[1]);
+        mma(qk[1], aq, bb[2], bb[3]);
+      }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (2 * wn + i <= wm) {
-          uint32_t bb[4];
-          ldsm4(bb, b_addr(ks, 32 * wn + 16 * i, k0, NB, lane));
-          mma(kk[2 * i], ak, bb[0], bb[1]);
-          mma(kk[2 * i + 1], ak, bb[2], bb[3]);
-          mma(qk[2 * i], aq, bb[0], bb[1]);
-          mma(qk[2 * i + 1], aq, bb[2], bb[3]);
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          kk2[y][r] = pack(kk[y][2 * r], kk[y][2 * r + 1]);
+          qk2[y][r] = pack(qk[y][2 * r], qk[y][2 * r + 1]);
         }
     }
-#pragma unroll
-    for (int y = 0; y < 4; ++y)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        kk2[y][r] = pack(kk[y][2 * r], kk[y][2 * r + 1]);
-        qk2[y][r] = pack(qk[y][2 * r], qk[y][2 * r + 1]);
-      }
   }
   // this thread's pair of k or q: rows[r], columns n0 + 8 y + c2
   auto pair_of = [&](const uint8_t *tile, int r, int y) {
@@ -288,51 +242,53 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
   float dq[2 * kPairs][4] = {}, dk[2 * kPairs][4] = {};
   for (int i = 0; i < s.hpg; ++i) {
     const int x = i & 1;
-    const float *vec = sm.vec[x];
+    const float *vec = sm.vec[i % 3];
     const uint32_t Xs = smem_at(sm.X[x]), Fs = smem_at(sm.F[x]), Es = smem_at(sm.E[x]);
-    __syncthreads();   // this head's rows are here
+    cp_wait<0>();
+    __syncthreads();   // this head's rows are here, the head before is done
+    const int64_t st = (slot * s.H + grp * s.hpg + i) * P * N;
+    copy(Ds, o.D16 + st, P * N / 8);
+    copy(Ss, t.S16 + st, P * N / 8);
+    cp_commit();
+    if (i + 1 < s.hpg) fetch_rows(i + 1);
+    else cp_commit();   // (a group all the same: the wait below counts them)
     const float ka = vec[kVecKa];
     const bool even = sm.even[x];
-    {
-      // blocks above the diagonal go along: a branch would cost more than they do
-      float n1[4][4] = {}, n2[4][4] = {};
-#pragma unroll 2
+    if (wn <= wm) {
+      float n1[2][4] = {}, n2[2][4] = {};
+#pragma unroll 4
       for (int j = 0; j < strips; ++j) {
-        uint32_t aX[4], aF[4], bb[2][4];
+        uint32_t aX[4], aF[4], bb[4];
         ldsm4(aX, block(Xs + arow, j));
         ldsm4(aF, block(Fs + arow, j));
-        ldsm4(bb[0], block(Es + brow, j));
-        ldsm4(bb[1], block(Es + brow, j) + 16 * kRow);
+        ldsm4(bb, block(Es + brow, j));
         if (!even) {
           const uint32_t f = twice(sm.rel[x][j]);
           scale_a(aX, f, f);
           scale_a(aF, f, f);
         }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          mma(n1[2 * y], aF, bb[y][0], bb[y][1]);
-          mma(n1[2 * y + 1], aF, bb[y][2], bb[y][3]);
-          mma(n2[2 * y], aX, bb[y][0], bb[y][1]);
-          mma(n2[2 * y + 1], aX, bb[y][2], bb[y][3]);
-        }
+        mma(n1[0], aF, bb[0], bb[1]);
+        mma(n1[1], aF, bb[2], bb[3]);
+        mma(n2[0], aX, bb[0], bb[1]);
+        mma(n2[1], aX, bb[2], bb[3]);
       }
       const float Gr[2] = {vec[kVecG + rows[0]], vec[kVecG + rows[1]]};
       const float Lr[2] = {vec[kVecGl + rows[0]], vec[kVecGl + rows[1]]};
       const float w1[2] = {-ka * vec[kVecBeta + rows[0]], -ka * vec[kVecBeta + rows[1]]};
       const float w2 = ka * a.scale;
-      float wrow[2] = {0.f, 0.f}, wcol[8];
-      float2 Gc[4], Lc[4], be[4];   // all of them first: the stores below would hold back the loads after them
+      float wrow[2] = {0.f, 0.f}, wcol[4];
+      float2 Gc[2], Lc[2], be[2];   // all of them first: the stores below would hold back the loads after them
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int c = 32 * wn + 8 * y + c2;
+      for (int y = 0; y < 2; ++y) {
+        const int c = 16 * wn + 8 * y + c2;
         Gc[y] = *reinterpret_cast<const float2 *>(&vec[kVecG + c]);
         Lc[y] = *reinterpret_cast<const float2 *>(&vec[kVecGl + c]);
         be[y] = *reinterpret_cast<const float2 *>(&vec[kVecBeta + c]);
       }
-      uint32_t m1[4][2], m2[4][2];
+      uint32_t m1[2][2], m2[2][2];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int c = 32 * wn + 8 * y + c2;
+      for (int y = 0; y < 2; ++y) {
+        const int c = 16 * wn + 8 * y + c2;
         wcol[2 * y] = wcol[2 * y + 1] = 0.f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -353,24 +309,21 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
           wcol[2 * y + 1] += v1;
         }
       }
-      if (wn == wm >> 1 && (lane & 3) == (g >> 1)) {   // this thread has the diagonal's elements g and g + 8
-        const int y = 2 * (wm & 1);
-        const float(&lo)[4] = y ? n1[2] : n1[0];
-        const float(&hi)[4] = y ? n1[3] : n1[1];
-        sm.fe[x][rows[0]] = g & 1 ? lo[1] : lo[0];
-        sm.fe[x][rows[1]] = g & 1 ? hi[3] : hi[2];
+      if (wn == wm && (lane & 3) == (g >> 1)) {   // this thread has the diagonal's elements g and g + 8
+        sm.fe[x][rows[0]] = g & 1 ? n1[0][1] : n1[0][0];
+        sm.fe[x][rows[1]] = g & 1 ? n1[1][3] : n1[1][2];
       }
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+      for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t to = swz(rows[r], 4 * wn + y, 128) + 2 * c2;
+          const uint32_t to = swz(rows[r], 2 * wn + y, 128) + 2 * c2;
           *reinterpret_cast<uint32_t *>(sm.m1 + to) = m1[y][r];
           *reinterpret_cast<uint32_t *>(sm.m2 + to) = m2[y][r];
         }
-      // over this strip's 16 tokens: eight columns by eight lanes, halving what each still carries
+      // over this strip's 16 tokens: four columns by eight lanes, halving what each still carries
 #pragma unroll
-      for (int d = 4, lanes = 16; d > 0; d >>= 1, lanes >>= 1) {
+      for (int d = 2, lanes = 16; d > 0; d >>= 1, lanes >>= 1) {
         const bool up = lane & lanes;
 #pragma unroll
         for (int z = 0; z < d; ++z) {
@@ -378,15 +331,37 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
           wcol[z] = keep + __shfl_xor_sync(~0u, give, lanes);
         }
       }
-      // left with column 8 y + c2 + z, 2 y + z = g
-      sm.wcol[x][wm][32 * wn + 8 * (g >> 1) + c2 + (g & 1)] = wcol[0] * ka;
+      wcol[0] += __shfl_xor_sync(~0u, wcol[0], 4);
+      // left with column 8 y + c2 + z, 2 y + z = g / 2
+      if (!(g & 1)) sm.wcol[x][wm][16 * wn + 8 * (g >> 2) + c2 + ((g >> 1) & 1)] = wcol[0] * ka;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         wrow[r] = quad_sum(wrow[r]);
         if (c2 == 0) sm.wrow[x][wn][rows[r]] = wrow[r] * ka;
       }
+    } else if (i > 0 && warp == 8 + 1) {
+      finish(i - 1);
     }
+    cp_wait<1>();
     __syncthreads();   // M1 and M2 are here, and the states
+    {
+      // <S0, dS>: the same element of both at the same place
+      float sum = 0.f;
+      for (int y = tid; y < P * N / 8; y += kThreads) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(sm.S + 16 * y), v = *reinterpret_cast<const uint4 *>(sm.D + 16 * y);
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+        float acc = 0.f;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const float2 fu = unpack(uu[z]), fv = unpack(vv[z]);
+          acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
+        }
+        sum = fmaf(acc, sm.rel[x][y / (2 * N)], sum);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      if (lane == 0) sm.inner[x][warp] = sum;
+    }
     uint32_t fx[2], ff[2], fu[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -401,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       uint32_t nX[4], nF[4];   // the left operands a step ahead
       ldsm4(nX, Xs + arow);
       ldsm4(nF, Fs + arow);
-#pragma unroll 2
+#pragma unroll 4
       for (int j = 0; j < strips; ++j) {
         uint32_t aX[4], aF[4];
 #pragma unroll
@@ -429,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       float z[2 * kPairs][4] = {};
       uint32_t nE[4];
       ldsm4(nE, Es + arow);
-#pragma unroll 2
+#pragma unroll 4
       for (int j = 0; j < strips; ++j) {
         uint32_t aE[4];
 #pragma unroll
@@ -470,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       step_t<kPairs, false>(dk, dk, a2, a2, qs + j * 16 * NB, at);
     }
   }
-  __syncthreads();   // what the copying warp still has to finish
+  __syncthreads();
+  if (warp == 0) finish(s.hpg - 1);
   __nv_bfloat16 *oq = static_cast<__nv_bfloat16 *>(a.dq), *ok = static_cast<__nv_bfloat16 *>(a.dk);
 #pragma unroll
   for (int r = 0; r < 2; ++r)
