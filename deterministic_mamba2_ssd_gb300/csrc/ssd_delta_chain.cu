@@ -48,19 +48,21 @@ constexpr int kM = 2;         // warp products a strip is high
 constexpr int kRows = 16 * kM;
 constexpr int kBlock = kChunk * kRows * 2;   // bytes of a strip's part of v: 64 tokens x 32
 
-template <int N, int kTerms, int kStrips>
+// kLeft: blocks of what a chunk leaves beside the one that v (dO) came in.
+template <int N, int kTerms, int kStrips, int kLeft>
 struct Layout {
-  // chunks of tiles in shared memory, one of them worked on; of v (dO) one more is needed, since its largest value is
-  // looked at a chunk ahead
-  static constexpr int kStages = kStrips * kTerms < 4 ? 3 : 2, kRing = kStages + 1;
   static constexpr int kK = 0, kQ = kChunk * N * 2, kY = 2 * kQ, kP = kY + 8192 * kTerms, kVecAt = kP + 8192,
                        kStage = kVecAt + (kVecChain * 4 + 127) / 128 * 128;
-  // a strip's own space: ring of v or dO, then the left operands
+  // a strip's own space: the left operands, what it leaves, the ring of v or dO
   static constexpr int kRow = kRows * 128, kPlane = kRows * 2 * N;   // bytes of 64 tokens' and of the state's columns
-  static constexpr int kS = kRing * kBlock, kR = kS + kTerms * kPlane, kU = kR + kTerms * kRow, kW = kU + kRow,
-                       kMax = kW + kTerms * kRow, kStrip = kMax + 128;
-  static constexpr int kBytes = kStages * kStage + kStrips * kStrip;
-  static_assert(kBytes <= 232448, "more shared memory than a CTA can have");
+  static constexpr int kS = 0, kR = kTerms * kPlane, kU = kR + kTerms * kRow, kW = kU + kRow, kMax = kW + kTerms * kRow,
+                       kOut = kMax + 128, kIn = kOut + kLeft * kBlock;
+  // chunks of tiles in shared memory, one of them worked on; of v (dO) one more is needed, since its largest value is
+  // looked at a chunk ahead
+  static constexpr int kLimit = 232448;
+  static constexpr int kStages = 3 * kStage + kStrips * (kIn + 4 * kBlock) <= kLimit ? 3 : 2, kRing = kStages + 1;
+  static constexpr int kStrip = kIn + kRing * kBlock, kOwn = kStages * kStage, kBytes = kOwn + kStrips * kStrip;
+  static_assert(kBytes <= kLimit, "more shared memory than a CTA can have");
 };
 
 struct Chunk {
@@ -117,10 +119,9 @@ __device__ __forceinline__ void to_a(const float (&x)[4], const float (&y)[4], u
   }
 }
 
-// The chunk's tiles, copied by kThreads threads of which this is `tid`.
-template <int N, int kTerms, int kStrips, int kThreads>
+// The chunk's tiles, copied by kLoaders threads of which this is `tid`.
+template <class L, int N, int kTerms>
 __device__ __forceinline__ void fetch_tiles(const Shape &s, const Tiles &t, int64_t slot, int h, uint32_t stage, int tid) {
-  using L = Layout<N, kTerms, kStrips>;
   const int64_t kt = (slot * s.G + h / s.hpg) * kChunk * N, ht = slot * s.H + h;
   const uint8_t *K = reinterpret_cast<const uint8_t *>(t.K16 + kt) + 16 * tid;
   const uint8_t *Q = reinterpret_cast<const uint8_t *>(t.Q16 + kt) + 16 * tid;
@@ -128,24 +129,24 @@ __device__ __forceinline__ void fetch_tiles(const Shape &s, const Tiles &t, int6
   const uint8_t *P = reinterpret_cast<const uint8_t *>(t.P16 + ht * kTri) + 16 * tid;
   stage += 16 * tid;
 #pragma unroll 8
-  for (int i = 0; i < kChunk * N / 8; i += kThreads) {
+  for (int i = 0; i < kChunk * N / 8; i += kLoaders) {
     cp16(stage + L::kK + 16 * i, K + 16 * i);
     cp16(stage + L::kQ + 16 * i, Q + 16 * i);
   }
 #pragma unroll 8
-  for (int i = 0; i < 512 * kTerms; i += kThreads) cp16(stage + L::kY + 16 * i, Y + 16 * i);
+  for (int i = 0; i < 512 * kTerms; i += kLoaders) cp16(stage + L::kY + 16 * i, Y + 16 * i);
 #pragma unroll 8
-  for (int i = 0; i < 512; i += kThreads) cp16(stage + L::kP + 16 * i, P + 16 * i);
-  for (int i = tid; i < kVecChain / 4; i += kThreads)
+  for (int i = 0; i < 512; i += kLoaders) cp16(stage + L::kP + 16 * i, P + 16 * i);
+  for (int i = tid; i < kVecChain / 4; i += kLoaders)
     cp16(stage + L::kVecAt + 16 * (i - tid), reinterpret_cast<const uint8_t *>(t.vec + ht * kVec) + 16 * i);
 }
 
 // The strips' columns of the chunk's v or dO; tokens past the end and columns past the head are zero.
-template <int kStrips, int kThreads>
+template <int kStrips>
 __device__ __forceinline__ void fetch_rows(const Chunk &c, const __nv_bfloat16 *x, int64_t stride, int p0, int P, bool vec,
                                            uint32_t at, uint8_t *gat, int step, int tid) {
 #pragma unroll 2
-  for (int i = tid; i < kStrips * kChunk * 4; i += kThreads) {
+  for (int i = tid; i < kStrips * kChunk * 4; i += kLoaders) {
     const int strip = i >> 8, r = (i >> 2) & 63, j = i & 3, col = p0 + strip * kRows + 8 * j;
     const uint32_t to = strip * step + row_at(r, j);
     const bool on = r < c.n && col < P;
@@ -167,38 +168,42 @@ __device__ __forceinline__ float bf16_top(uint32_t m) {
   return __uint_as_float(__reduce_max_sync(~0u, max(m & 0xffffu, m >> 16)) << 16);
 }
 
-// What the copying warps do: the tiles of a chunk and the rows of the one after, a stage or two ahead, and each
-// strip's largest value of those rows, for which the chain would have to wait.
-template <int N, int kTerms, int kStrips, int kThreads, class Of>
+// What the copying warps do: the tiles of a chunk and the rows of the one after, a stage or two ahead; each strip's
+// largest value of those rows, for which the chain would have to wait; and with kHand what the chunk before has left,
+// and the state as it stands, to where they belong (`leave`).
+//
+// kHand is the rule for what one strip a CTA records for a backward: with one warp on a scheduler nothing hides those
+// stores (16384 tokens x 64 heads: forward 442 us with the chain's own stores, 392 so; backward 512, 490).  Two strips
+// hide one another's, and the chain's own stores win (4 x 2048 tokens x 32 heads: 187 and 222 us, 213 and 225 so).
+template <class L, int N, int kTerms, int kStrips, bool kHand, class Of, class Leave>
 __device__ __forceinline__ void copy_in(const Shape &s, const Tiles &t, const __nv_bfloat16 *x, int64_t stride, bool vec,
-                                        int h, int p0, int64_t nc, Of of, uint8_t *smem, int tid) {
-  using L = Layout<N, kTerms, kStrips>;
-  constexpr int kOwn = L::kStages * L::kStage;
+                                        int h, int p0, int64_t nc, Of of, Leave leave, uint8_t *smem) {
+  const int tid = threadIdx.x & (kLoaders - 1);
   const uint32_t base = smem_at(smem);
   auto rows = [&](int64_t c) {
     if (c < nc) {
-      const int at = kOwn + int(c % L::kRing) * kBlock;
-      fetch_rows<kStrips, kThreads>(of(c), x + h * s.P, stride, p0, s.P, vec, base + at, smem + at, L::kStrip, tid);
+      const int at = L::kOwn + L::kIn + int(c % L::kRing) * kBlock;
+      fetch_rows<kStrips>(of(c), x + h * s.P, stride, p0, s.P, vec, base + at, smem + at, L::kStrip, tid);
     }
   };
   auto tops = [&](int64_t c) {   // of the pieces that this thread has copied
 #pragma unroll
     for (int y = 0; y < kStrips; ++y) {
+      uint8_t *own = smem + L::kOwn + y * L::kStrip;
       uint32_t m = 0;
       if (c < nc)
 #pragma unroll
-        for (int i = 0; i < 256; i += kThreads) {
-          const int r = (i + tid) >> 2, j = tid & 3;
-          const uint4 v = *reinterpret_cast<const uint4 *>(smem + kOwn + y * L::kStrip + int(c % L::kRing) * kBlock + row_at(r, j));
+        for (int i = 0; i < 256; i += kLoaders) {
+          const uint4 v =
+              *reinterpret_cast<const uint4 *>(own + L::kIn + int(c % L::kRing) * kBlock + row_at((i + tid) >> 2, tid & 3));
           m = top2(top2(top2(top2(m, v.x), v.y), v.z), v.w);
         }
       const float top = bf16_top(m);
-      if ((tid & 31) == 0)
-        reinterpret_cast<float *>(smem + kOwn + y * L::kStrip + L::kMax)[8 + 4 * int(c & 1) + (tid >> 5)] = top;
+      if ((tid & 31) == 0) reinterpret_cast<float *>(own + L::kMax)[8 + 4 * int(c & 1) + (tid >> 5)] = top;
     }
   };
   auto fetch = [&](int64_t c) {
-    if (c < nc) fetch_tiles<N, kTerms, kStrips, kThreads>(s, t, of(c).slot, h, base + int(c % L::kStages) * L::kStage, tid);
+    if (c < nc) fetch_tiles<L, N, kTerms>(s, t, of(c).slot, h, base + int(c % L::kStages) * L::kStage, tid);
     rows(c + 1);
     cp_commit();
   };
@@ -213,9 +218,37 @@ __device__ __forceinline__ void copy_in(const Shape &s, const Tiles &t, const __
     cp_wait<L::kStages - 2>();
     tops(c + 1);
     __syncthreads();   // tiles of c, rows of c + 1 are here; everyone is done with chunk c - 1
+    if constexpr (kHand) {
+      // the chain's first products want all of shared memory's bandwidth
+      asm volatile("bar.sync 7, %0;" ::"n"(128 * kStrips + kLoaders) : "memory");
+      leave(c);
+      asm volatile("bar.arrive 6, %0;" ::"n"(128 * kStrips + kLoaders) : "memory");   // the state's space and those blocks are free
+      asm volatile("bar.sync 5, %0;" ::"n"(kLoaders) : "memory");                     // also for the rows that come in there
+    }
     fetch(c + L::kStages - 1);
   }
   cp_wait<0>();
+  if constexpr (kHand) {
+    __syncthreads();
+    leave(nc);
+  }
+}
+// The chain's side of `leave`: before the blocks and the state's space are written again.
+template <int kStrips, bool kHand>
+__device__ __forceinline__ void left_sync() {
+  if constexpr (kHand) asm volatile("bar.sync 6, %0;" ::"n"(128 * kStrips + kLoaders) : "memory");
+}
+// ...and after its first products.
+template <int kStrips, bool kHand>
+__device__ __forceinline__ void first_done() {
+  if constexpr (kHand) asm volatile("bar.arrive 7, %0;" ::"n"(128 * kStrips + kLoaders) : "memory");
+}
+// One of the copying warps' threads, of 16-byte piece `i` of a block: its token, column and place.
+struct Piece {
+  int tok, col, at;
+};
+__device__ __forceinline__ Piece piece_of(int i) {
+  return {i >> 2, 8 * (i & 3), int(row_at(i >> 2, i & 3))};
 }
 
 __device__ __forceinline__ void put_out(__nv_bfloat16 *p, bool vec, uint4 v) {
@@ -231,12 +264,16 @@ __device__ __forceinline__ void put_out(__nv_bfloat16 *p, bool vec, uint4 v) {
   }
 }
 
-// This warp's 16 tokens x 32 rows through its part of a block to [token][row]: the lane's 16 bytes of either tile.
+// This warp's 16 tokens x 32 rows to its part of a block, [token][row]; `turned`: and back, the lane's 16 bytes of
+// either tile.
+__device__ __forceinline__ void put_block(uint32_t blk, const uint32_t (&x)[kM][4], int w, int lane) {
+#pragma unroll
+  for (int m = 0; m < kM; ++m) stsm4t(block_addr(blk, w, 7 - w, m, lane), x[m]);
+}
 __device__ __forceinline__ void turned(uint4 (&v)[2], uint8_t *gblock, uint32_t blk, const uint32_t (&x)[kM][4], int w,
                                        int lane) {
   __syncwarp();
-#pragma unroll
-  for (int m = 0; m < kM; ++m) stsm4t(block_addr(blk, w, 7 - w, m, lane), x[m]);
+  put_block(blk, x, w, lane);
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -362,12 +399,22 @@ __device__ __forceinline__ uint32_t put_state(const float (&S)[kM][kTiles][4], u
     }
   return top;
 }
+// The state as it stands in shared memory, `rows` of a strip's, to a record: contiguous there too.
+template <int N>
+__device__ __forceinline__ void copy_state(const uint8_t *from, __half *to, int rows) {
+#pragma unroll
+  for (int i = 0; i < kRows * N / 8; i += kLoaders) {
+    const int at = i + (threadIdx.x & (kLoaders - 1));
+    if (at < rows * N / 8) *reinterpret_cast<uint4 *>(to + 8 * at) = *reinterpret_cast<const uint4 *>(from + 16 * at);
+  }
+}
 
 // CTA (kStrips strips of 32 rows, head, sequence): four warps a strip, and the warps that copy.
 template <int N, int kTerms, int kStrips, bool kSave>
 __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(Shape s, Args a, Tiles t, int vvec,
                                                                                           int ovec) {
-  using L = Layout<N, kTerms, kStrips>;
+  constexpr bool kHand = kSave && kStrips == 1;
+  using L = Layout<N, kTerms, kStrips, kHand ? 1 : 0>;
   constexpr int kTiles = N / 32, NB = 2 * N;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
@@ -379,16 +426,36 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
   auto chunk = [&](int64_t c) {
     return Chunk{slot0 + c, t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
   };
+  __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
   if (strip == kStrips) {
-    copy_in<N, kTerms, kStrips, kLoaders>(s, t, static_cast<const __nv_bfloat16 *>(a.v), s.vs, vvec, h,
-                                                    int(blockIdx.x) * kStrips * kRows, nc, chunk, smem, threadIdx.x & 127);
+    auto leave = [&](int64_t c) {
+#pragma unroll
+      for (int y = 0; y < kStrips; ++y) {
+        const int p = (blockIdx.x * kStrips + y) * kRows, rows = s.P - p;
+        const uint8_t *own = smem + L::kOwn + y * L::kStrip;
+        if (c < nc) copy_state<N>(own + L::kS, t.S16 + (((slot0 + c) * s.H + h) * s.P + p) * N, rows);
+        if (c == 0) continue;
+        const Chunk ck = chunk(c - 1);
+#pragma unroll
+        for (int i = 0; i < 256; i += kLoaders) {
+          const Piece x = piece_of(i + (threadIdx.x & (kLoaders - 1)));
+          if (x.col >= rows) continue;
+          if (x.tok < ck.n)
+            put_out(o + ((ck.b + x.tok) * s.H + h) * s.P + p + x.col, ovec,
+                    *reinterpret_cast<const uint4 *>(own + L::kIn + int((c - 1) % L::kRing) * kBlock + x.at));
+          *reinterpret_cast<uint4 *>(t.E16 + ((ck.slot * s.H + h) * kChunk + x.tok) * s.P + p + x.col) =
+              *reinterpret_cast<const uint4 *>(own + L::kOut + x.at);
+        }
+      }
+    };
+    copy_in<L, N, kTerms, kStrips, kHand>(s, t, static_cast<const __nv_bfloat16 *>(a.v), s.vs, vvec, h,
+                                   int(blockIdx.x) * kStrips * kRows, nc, chunk, leave, smem);
     return;
   }
   const int rows = s.P - p0;
   const bool live = rows > 0;
-  __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
-  const uint32_t base = smem_at(smem), own = base + L::kStages * L::kStage + strip * L::kStrip;
-  uint8_t *gown = smem + L::kStages * L::kStage + strip * L::kStrip;
+  const uint32_t base = smem_at(smem), own = base + L::kOwn + strip * L::kStrip;
+  uint8_t *gown = smem + L::kOwn + strip * L::kStrip;
   float *mx = reinterpret_cast<float *>(gown + L::kMax);
   const uint32_t Srow = own + L::kS + left_row(lane, NB), Rrow = own + L::kR + left_row(lane, 128),
                  Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128),
@@ -401,7 +468,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
   // v of chunk c, this warp's tokens, as packed pairs
   auto load_v = [&](uint32_t (&x)[kM][4], int64_t c) {
 #pragma unroll
-    for (int m = 0; m < kM; ++m) ldsm4t(x[m], block_addr(own + int(c % L::kRing) * kBlock, w, 7 - w, m, lane));
+    for (int m = 0; m < kM; ++m) ldsm4t(x[m], block_addr(own + L::kIn + int(c % L::kRing) * kBlock, w, 7 - w, m, lane));
   };
   if (nc > 0) {
     __syncthreads();
@@ -417,14 +484,17 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
     const int64_t ht = ck.slot * s.H + h;
     uint32_t top = 0;
     if (live) {
-      top = put_state<N, kTerms, kSave>(S, Srow, L::kPlane, w * (N / 64), kSave ? t.S16 + (ht * s.P + p0) * N : nullptr, rows,
-                                        lane);
+      top = put_state<N, kTerms, kSave && !kHand>(S, Srow, L::kPlane, w * (N / 64), t.S16 + (ht * s.P + p0) * N, rows, lane);
       if (kSave && (threadIdx.x & 127) < kM && 16 * (threadIdx.x & 127) < rows)
         t.up[((ht * s.P + p0) >> 4) + (threadIdx.x & 127)] = sc.up;
     }
     __syncthreads();   // tiles of c, rows of c + 1, S of every warp
-    if (!live) continue;
-    const int stage = int(c % L::kStages) * L::kStage, ring = int(c % L::kRing) * kBlock;
+    if (!live) {
+      first_done<kStrips, kHand>();
+      left_sync<kStrips, kHand>();
+      continue;
+    }
+    const int stage = int(c % L::kStages) * L::kStage, ring = L::kIn + int(c % L::kRing) * kBlock;
     const uint32_t tiles = base + stage;
     const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
     const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1];
@@ -446,6 +516,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         if (kTerms == 2) mul(R, 0, sa[kTerms - 1], kb);
       }
     }
+    first_done<kStrips, kHand>();
     float2 be[2];
     {
       uint32_t vw[kM][4];
@@ -583,30 +654,37 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         mul(O, 0, ua, pb, kStrips > 1 ? 2 * j <= w : j < 2);
       }
     }
-    // outputs and record through this warp's tokens of the v block, which it alone has read
+    // outputs take the place of v, whose tokens each warp alone has read
     const float co = a.scale * ka * sc.up;
     uint32_t ow[kM][4];
 #pragma unroll
     for (int m = 0; m < kM; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) ow[m][i] = pack_bf16(O[m][i >> 1][2 * (i & 1)] * co, O[m][i >> 1][2 * (i & 1) + 1] * co);
-    uint4 out[2];
-    turned(out, gown + ring, own + ring, ow, w, lane);
-    const int col = 8 * (lane & 3);
+    if constexpr (kHand) {
+      put_block(own + ring, ow, w, lane);
+      left_sync<kStrips, kHand>();
+      put_block(own + L::kOut, ew, w, lane);
+    } else {
+      const int col = 8 * (lane & 3);
+      uint4 out[2];
+      turned(out, gown + ring, own + ring, ow, w, lane);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int tok = 8 * tile_of(w, i) + (lane >> 2);
-      if (tok < ck.n && col < rows) put_out(o + ((ck.b + tok) * s.H + h) * s.P + p0 + col, ovec, out[i]);
-    }
-    if (kSave) {
-      turned(out, gown + ring, own + ring, ew, w, lane);
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 8 * tile_of(w, i) + (lane >> 2);
+        if (tok < ck.n && col < rows) put_out(o + ((ck.b + tok) * s.H + h) * s.P + p0 + col, ovec, out[i]);
+      }
+      if (kSave) {
+        turned(out, gown + ring, own + ring, ew, w, lane);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (col < rows)
-          *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + 8 * tile_of(w, i) + (lane >> 2)) * s.P + p0 + col) = out[i];
+        for (int i = 0; i < 2; ++i)
+          if (col < rows)
+            *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + 8 * tile_of(w, i) + (lane >> 2)) * s.P + p0 + col) = out[i];
+      }
     }
     sc.move(S, f);
   }
+  if (kHand && nc > 0) __syncthreads();   // the last chunk's outputs
   if (live && a.fin != nullptr) store_state<kTiles>(S, a.fin + row, sc.up, rows, N, lane);
 }
 
@@ -614,7 +692,8 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
 template <int N, int kStrips>
 __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(Shape s, Args a, Tiles t,
                                                                                           BwdTiles o, int gvec, int ovec) {
-  using L = Layout<N, 1, kStrips>;
+  constexpr bool kHand = kStrips == 1;
+  using L = Layout<N, 1, kStrips, kHand ? 2 : 0>;
   constexpr int kTiles = N / 32, NB = 2 * N;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3;
@@ -628,16 +707,38 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
     const int64_t c = nc - 1 - i;
     return Chunk{slot0 + c, t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
   };
+  __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv);
   if (strip == kStrips) {
-    copy_in<N, 1, kStrips, kLoaders>(s, t, static_cast<const __nv_bfloat16 *>(a.dout), tok_stride, gvec, h,
-                                               int(blockIdx.x) * kStrips * kRows, nc, chunk, smem, threadIdx.x & 127);
+    auto leave = [&](int64_t c) {
+#pragma unroll
+      for (int y = 0; y < kStrips; ++y) {
+        const int p = (blockIdx.x * kStrips + y) * kRows, rows = s.P - p;
+        const uint8_t *own = smem + L::kOwn + y * L::kStrip;
+        if (c < nc) copy_state<N>(own + L::kS, o.D16 + ((chunk(c).slot * s.H + h) * s.P + p) * N, rows);
+        if (c == 0) continue;
+        const Chunk ck = chunk(c - 1);
+#pragma unroll
+        for (int i = 0; i < 256; i += kLoaders) {
+          const Piece x = piece_of(i + (threadIdx.x & (kLoaders - 1)));
+          if (x.col >= rows) continue;
+          const int64_t at = ((ck.slot * s.H + h) * kChunk + x.tok) * s.P + p + x.col;
+          *reinterpret_cast<uint4 *>(o.X16 + at) =
+              *reinterpret_cast<const uint4 *>(own + L::kIn + int((c - 1) % L::kRing) * kBlock + x.at);
+          *reinterpret_cast<uint4 *>(o.F16 + at) = *reinterpret_cast<const uint4 *>(own + L::kOut + x.at);
+          if (x.tok < ck.n)
+            put_out(dv + (ck.b + x.tok) * tok_stride + h * s.P + p + x.col, ovec,
+                    *reinterpret_cast<const uint4 *>(own + L::kOut + kBlock + x.at));
+        }
+      }
+    };
+    copy_in<L, N, 1, kStrips, kHand>(s, t, static_cast<const __nv_bfloat16 *>(a.dout), tok_stride, gvec, h,
+                              int(blockIdx.x) * kStrips * kRows, nc, chunk, leave, smem);
     return;
   }
   const int rows = s.P - p0;
   const bool live = rows > 0;
-  __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv);
-  const uint32_t base = smem_at(smem), own = base + L::kStages * L::kStage + strip * L::kStrip;
-  uint8_t *gown = smem + L::kStages * L::kStage + strip * L::kStrip;
+  const uint32_t base = smem_at(smem), own = base + L::kOwn + strip * L::kStrip;
+  uint8_t *gown = smem + L::kOwn + strip * L::kStrip;
   float *mx = reinterpret_cast<float *>(gown + L::kMax);
   const uint32_t Srow = own + L::kS + left_row(lane, NB), Rrow = own + L::kR + left_row(lane, 128),
                  Urow = own + L::kU + left_row(lane, 128), Wrow = own + L::kW + left_row(lane, 128),
@@ -651,7 +752,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
   auto take_x = [&](int64_t c) {
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
-      const uint32_t at = block_addr(own + int(c % L::kRing) * kBlock, w, 7 - w, m, lane);
+      const uint32_t at = block_addr(own + L::kIn + int(c % L::kRing) * kBlock, w, 7 - w, m, lane);
       uint32_t x[4];
       ldsm4t(x, at);
 #pragma unroll
@@ -677,12 +778,16 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
     const int64_t ht = ck.slot * s.H + h;
     uint32_t top = 0;
     if (live) {
-      top = put_state<N, 1, true>(D, Srow, L::kPlane, w * (N / 64), o.D16 + (ht * s.P + p0) * N, rows, lane);
+      top = put_state<N, 1, !kHand>(D, Srow, L::kPlane, w * (N / 64), o.D16 + (ht * s.P + p0) * N, rows, lane);
       if ((threadIdx.x & 127) < kM && 16 * (threadIdx.x & 127) < rows) o.ub[((ht * s.P + p0) >> 4) + (threadIdx.x & 127)] = sc.up;
     }
     __syncthreads();   // tiles of c, rows of c + 1, dS and dO of every warp
-    if (!live) continue;
-    const int stage = int(c % L::kStages) * L::kStage, ring = int(c % L::kRing) * kBlock;
+    if (!live) {
+      first_done<kStrips, kHand>();
+      left_sync<kStrips, kHand>();
+      continue;
+    }
+    const int stage = int(c % L::kStages) * L::kStage, ring = L::kIn + int(c % L::kRing) * kBlock;
     const uint32_t tiles = base + stage;
     const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
     const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1], co = a.scale * ka;
@@ -699,6 +804,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
         mul(F, 0, da, kb);
       }
     }
+    first_done<kStrips, kHand>();
     float2 be[2], eg[2];
     {
       float A[kM][2][4] = {};
@@ -823,28 +929,35 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
           rw[m][2 * i + r] = pack(f0, f1);
           vw[m][2 * i + r] = pack_bf16(f0 * (be[i].x * sc.up), f1 * (be[i].y * sc.up));
         }
-    const int col = 8 * (lane & 3);
-    auto at = [&](int i) { return (ht * kChunk + 8 * tile_of(w, i) + (lane >> 2)) * s.P + p0 + col; };
-    uint4 out[2];
-    // every warp has read dO's tiles by the last barrier: this warp's tokens of the block are its own
+    if constexpr (kHand) {
+      left_sync<kStrips, kHand>();
+      put_block(own + L::kOut, rw, w, lane);
+      put_block(own + L::kOut + kBlock, vw, w, lane);
+    } else {
+      const int col = 8 * (lane & 3);
+      auto at = [&](int i) { return (ht * kChunk + 8 * tile_of(w, i) + (lane >> 2)) * s.P + p0 + col; };
+      uint4 out[2];
+      // every warp has read dO's tiles by the last barrier: this warp's tokens of the block are its own
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (col < rows)
-        *reinterpret_cast<uint4 *>(o.X16 + at(i)) =
-            *reinterpret_cast<const uint4 *>(gown + ring + row_at(8 * tile_of(w, i) + (lane >> 2), lane & 3));
-    turned(out, gown + ring, own + ring, rw, w, lane);
+      for (int i = 0; i < 2; ++i)
+        if (col < rows)
+          *reinterpret_cast<uint4 *>(o.X16 + at(i)) =
+              *reinterpret_cast<const uint4 *>(gown + ring + row_at(8 * tile_of(w, i) + (lane >> 2), lane & 3));
+      turned(out, gown + ring, own + ring, rw, w, lane);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (col < rows) *reinterpret_cast<uint4 *>(o.F16 + at(i)) = out[i];
-    turned(out, gown + ring, own + ring, vw, w, lane);
+      for (int i = 0; i < 2; ++i)
+        if (col < rows) *reinterpret_cast<uint4 *>(o.F16 + at(i)) = out[i];
+      turned(out, gown + ring, own + ring, vw, w, lane);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int tok = 8 * tile_of(w, i) + (lane >> 2);
-      if (tok < ck.n && col < rows) put_out(dv + (ck.b + tok) * tok_stride + h * s.P + p0 + col, ovec, out[i]);
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 8 * tile_of(w, i) + (lane >> 2);
+        if (tok < ck.n && col < rows) put_out(dv + (ck.b + tok) * tok_stride + h * s.P + p0 + col, ovec, out[i]);
+      }
     }
     sc.move(D, f);
     if (c + 1 < nc) take_x(c + 1);
   }
+  if (kHand && nc > 0) __syncthreads();
   if (live && a.dinit != nullptr) store_state<kTiles>(D, a.dinit + row, sc.up, rows, N, lane);
 }
 
@@ -863,7 +976,7 @@ dim3 chain_grid(const Shape &s, int n) {
 template <int N, int kTerms, int kStrips, bool kSave>
 cudaError_t go_fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) {
   auto kernel = chain_fwd_kernel<N, kTerms, kStrips, kSave>;
-  constexpr int smem = Layout<N, kTerms, kStrips>::kBytes;
+  constexpr int smem = Layout<N, kTerms, kStrips, kSave && kStrips == 1 ? 1 : 0>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<chain_grid(s, kStrips), 128 * kStrips + kLoaders, smem, st>>>(s, a, t, vec16(a.v, s.vs), vec16(a.o, 8));
@@ -885,7 +998,7 @@ cudaError_t fwd(const Shape &s, const Args &a, const Tiles &t, cudaStream_t st) 
 template <int N, int kStrips>
 cudaError_t go_bwd(const Shape &s, const Args &a, const Tiles &t, const BwdTiles &b, cudaStream_t st) {
   auto kernel = chain_bwd_kernel<N, kStrips>;
-  constexpr int smem = Layout<N, 1, kStrips>::kBytes;
+  constexpr int smem = Layout<N, 1, kStrips, kStrips == 1 ? 2 : 0>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<chain_grid(s, kStrips), 128 * kStrips + kLoaders, smem, st>>>(s, a, t, b, vec16(a.dout, 8), vec16(a.dv, 8));
