@@ -42,7 +42,7 @@ namespace {
 
 using namespace mma16;
 
-constexpr float kLow = 0.25f, kHigh = 64.f;   // window of a strip's largest value
+constexpr float kLow = 0.25f;   // a strip's largest value is kept from kLow to 2^8 kLow
 constexpr int kLoaders = 128;                 // threads that copy
 constexpr int kM = 2;         // warp products a strip is high
 constexpr int kRows = 16 * kM;
@@ -104,16 +104,35 @@ __device__ __forceinline__ uint32_t turned_row(int w, int lane) {
 }
 __device__ __forceinline__ uint32_t block(uint32_t row, int j) { return (row ^ ((j & 3) << 5)) + ((j >> 2) << 7); }
 
+// (a, b) as fp16 plus, with kTerms 2, 2^11 times what the first rounding left over: so far up, the second term is not
+// cut off by fp16's smallest number.  Its right operand goes down by as much (`lowered`).
+template <int kTerms>
+__device__ __forceinline__ void split_up(float a, float b, uint32_t (&out)[kTerms]) {
+  out[0] = pack(a, b);
+  if constexpr (kTerms == 2) {
+    const float2 h = unpack(out[0]);
+    out[1] = pack((a - h.x) * 2048.f, (b - h.y) * 2048.f);
+  }
+}
+__device__ __forceinline__ void lowered(uint32_t (&to)[4], const uint32_t (&b)[4]) {
+  const __half2 f = __float2half2_rn(1.f / 2048.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&b[i]), f);
+    to[i] = *reinterpret_cast<const uint32_t *>(&v);
+  }
+}
+
 // 16 x 16 values (two accumulator tiles) rounded, as the four matrices of a store.
 template <int kTerms>
 __device__ __forceinline__ void to_a(const float (&x)[4], const float (&y)[4], uint32_t (&a)[kTerms][4]) {
   uint32_t p[kTerms];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    split<kTerms>(x[2 * i], x[2 * i + 1], p);
+    split_up<kTerms>(x[2 * i], x[2 * i + 1], p);
 #pragma unroll
     for (int t = 0; t < kTerms; ++t) a[t][i] = p[t];
-    split<kTerms>(y[2 * i], y[2 * i + 1], p);
+    split_up<kTerms>(y[2 * i], y[2 * i + 1], p);
 #pragma unroll
     for (int t = 0; t < kTerms; ++t) a[t][2 + i] = p[t];
   }
@@ -299,8 +318,9 @@ __device__ __forceinline__ float state_top(const float (&S)[kM][kTiles][4]) {
 // Factor that brings a strip's largest value `need` back into the window (1 while it is inside, zero or not finite).
 // A power of 2^8, so that strips of like size share one scale and the gradient kernel has nothing to adjust.
 __device__ __forceinline__ float rescale(float need, float dn) {
-  if (!(need > kHigh || (need < kLow && need > 0.f)) || isinf(need)) return 1.f;
-  const int e = int(__float_as_uint(need) >> 23) - 127 + 2;   // need = 2^-2 2^e (1 to 2)
+  need *= 1.f / kLow;
+  if (!(need > 256.f || (need < 1.f && need > 0.f)) || isinf(need)) return 1.f;
+  const int e = int(__float_as_uint(need) >> 23) - 127;   // need = 2^e (1 to 2)
   const int k = e >= 0 ? e / 8 : (e - 7) / 8;
   const float f = __uint_as_float(uint32_t(127 - 8 * max(-12, min(12, k))) << 23);
   const float lim = 1.0e33f;   // keeps both scales finite
@@ -463,6 +483,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
                  Wput = own + L::kW + turned_row(w, lane);
   float S[kM][kTiles][4];
   Scaled<kTiles> sc;
+  float unit = 1.f;   // of S beside the scale: 16 2^a of the chunk before, so that W and K16 need no factor
   const int64_t row = ((seq * s.H + h) * s.P + p0) * N + n0;
   load_state<kTiles>(S, a.init + row, a.init != nullptr ? rows : 0, N, lane);
   // v of chunk c, this warp's tokens, as packed pairs
@@ -487,6 +508,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
       top = put_state<N, kTerms, kSave && !kHand>(S, Srow, L::kPlane, w * (N / 64), t.S16 + (ht * s.P + p0) * N, rows, lane);
       if (kSave && (threadIdx.x & 127) < kM && 16 * (threadIdx.x & 127) < rows)
         t.up[((ht * s.P + p0) >> 4) + (threadIdx.x & 127)] = sc.up;
+      if (kSave && p0 == 0 && (threadIdx.x & 127) == 0) t.vec[ht * kVec + kVecUnit] = unit;
     }
     __syncthreads();   // tiles of c, rows of c + 1, S of every warp
     if (!live) {
@@ -497,7 +519,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
     const int stage = int(c % L::kStages) * L::kStage, ring = L::kIn + int(c % L::kRing) * kBlock;
     const uint32_t tiles = base + stage;
     const float *vec = reinterpret_cast<const float *>(smem + stage + L::kVecAt);
-    const float ka = vec[kVecKa], last = vec[kVecEg + kChunk - 1];
+    const float ka = vec[kVecKa], ika = pow2_inv(ka), keep = vec[kVecEg + kChunk - 1] * (unit * (ika * 0.0625f));
     const float2 eg[2] = {vec2(vec + kVecEg, w, 0, lane), vec2(vec + kVecEg, w, 1, lane)};
     float R[kM][2][4] = {}, O[kM][2][4] = {};
     {
@@ -513,7 +535,10 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         ldsm4(qb, block(krow, j) + (L::kQ - L::kK));
         mul(R, 0, sa[0], kb);   // an accumulator's products four or more apart
         mul(O, 0, sa[0], qb);
-        if (kTerms == 2) mul(R, 0, sa[kTerms - 1], kb);
+        if constexpr (kTerms == 2) {
+          lowered(kb, kb);
+          mul(R, 0, sa[1], kb);
+        }
       }
     }
     first_done<kStrips, kHand>();
@@ -529,7 +554,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         uint32_t ra[kTerms][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float c0 = eg[i].x * ka, c1 = eg[i].y * ka;
+          const float c0 = eg[i].x * (ka * unit), c1 = eg[i].y * (ka * unit);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float2 v = unpack_bf16(vw[m][2 * i + r]);
@@ -564,9 +589,10 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         }
         const bool on = kStrips > 1 ? 2 * j <= w : j < 2;
         mul(E, 0, ra[0], yb[0], on);
-        if (kTerms == 2) {
-          mul(kApart ? E2 : E, 0, ra[kTerms - 1], yb[0], on);
-          mul(kApart ? E2 : E, 0, ra[0], yb[kTerms - 1], on);
+        if constexpr (kTerms == 2) {
+          mul(kApart ? E2 : E, 0, ra[0], yb[1], on);
+          lowered(yb[0], yb[0]);
+          mul(kApart ? E2 : E, 0, ra[1], yb[0], on);
         }
       }
       if (kApart)
@@ -579,6 +605,8 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
       for (int i = 0; i < 2; ++i) {
         tau[i] = vec2(vec + kVecTau, w, i, lane);
         tl[i] = vec2(vec + kVecTail, w, i, lane);
+        tl[i].x *= 0.0625f;
+        tl[i].y *= 0.0625f;
       }
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
@@ -589,8 +617,8 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
           for (int r = 0; r < 4; r += 2) {
             const float e0 = fmaf(-tau[i].x, E[m][i][r], R[m][i][r]), e1 = fmaf(-tau[i].y, E[m][i][r + 1], R[m][i][r + 1]);
             if (kSave) ew[m][2 * i + r / 2] = pack(e0, e1);
-            E[m][i][r] = e0 * (be[i].x * ka);
-            E[m][i][r + 1] = e1 * (be[i].y * ka);
+            E[m][i][r] = e0 * be[i].x;
+            E[m][i][r + 1] = e1 * be[i].y;
             W[i][r] = E[m][i][r] * tl[i].x;
             W[i][r + 1] = E[m][i][r + 1] * tl[i].y;
           }
@@ -613,15 +641,15 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[m][i][r] *= last;
+        for (int r = 0; r < 4; ++r) S[m][i][r] *= keep;
 #pragma unroll
     for (int m = 0; m < kM; ++m)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 4; r += 2) {
-          O[m][i][r] *= eg[i].x;
-          O[m][i][r + 1] *= eg[i].y;
+          O[m][i][r] *= eg[i].x * (unit * ika);
+          O[m][i][r + 1] *= eg[i].y * (unit * ika);
         }
     strip_sync(strip);
     const float f = rescale(fmaxf(strip_top(mx + 4 * (c & 1)), strip_top(mx + 8 + 4 * ((c + 1) & 1)) * sc.dn), sc.dn);
@@ -637,9 +665,13 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
 #pragma unroll
         for (int i = 0; i < kTiles / 2; ++i) ldsm4t(kb[i], (kcol ^ (i << 5)) + j * 16 * NB);
 #pragma unroll
-        for (int x = 0; x < kTerms; ++x)
+        for (int i = 0; i < kTiles / 2; ++i) mul(S, 2 * i, wa[0], kb[i]);
+        if constexpr (kTerms == 2)
 #pragma unroll
-          for (int i = 0; i < kTiles / 2; ++i) mul(S, 2 * i, wa[x], kb[i]);
+          for (int i = 0; i < kTiles / 2; ++i) {
+            lowered(kb[i], kb[i]);
+            mul(S, 2 * i, wa[1], kb[i]);
+          }
       }
     }
     {
@@ -655,7 +687,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
       }
     }
     // outputs take the place of v, whose tokens each warp alone has read
-    const float co = a.scale * ka * sc.up;
+    const float co = a.scale * (ka * ka) * sc.up;
     uint32_t ow[kM][4];
 #pragma unroll
     for (int m = 0; m < kM; ++m)
@@ -682,10 +714,11 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
             *reinterpret_cast<uint4 *>(t.E16 + (ht * kChunk + 8 * tile_of(w, i) + (lane >> 2)) * s.P + p0 + col) = out[i];
       }
     }
+    unit = 16.f * ka;
     sc.move(S, f);
   }
   if (kHand && nc > 0) __syncthreads();   // the last chunk's outputs
-  if (live && a.fin != nullptr) store_state<kTiles>(S, a.fin + row, sc.up, rows, N, lane);
+  if (live && a.fin != nullptr) store_state<kTiles>(S, a.fin + row, sc.up * unit, rows, N, lane);
 }
 
 // The reverse recurrence; writes dv, dinit, and for the gradient kernel dS leaving each chunk (D16), F (F16) and dO (X16).

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
     float from[2], cut[2], dn[2], inner = lane < kThreads / 32 ? sm.inner[x][lane] : 0.f;
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) inner += __shfl_xor_sync(~0u, inner, d);
-    inner = __shfl_sync(~0u, inner, 0) * sm.vec[i % 3][kVecEg + kChunk - 1];
+    inner = __shfl_sync(~0u, inner, 0) * (sm.vec[i % 3][kVecEg + kChunk - 1] * sm.vec[i % 3][kVecUnit]);
     auto four = [](const float (&v)[4][kChunk], int r) { return (v[0][r] + v[1][r]) + (v[2][r] + v[3][r]); };
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
         wcol[2 * y] = wcol[2 * y + 1] = 0.f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float d0 = __expf(acs_diff(Gr[r], Lr[r], Gc[y].x, Lc[y].x)) * be[y].x;
-          const float d1 = __expf(acs_diff(Gr[r], Lr[r], Gc[y].y, Lc[y].y)) * be[y].y;
+          const float d0 = exp2f(acs_diff(Gr[r], Lr[r], Gc[y].x, Lc[y].x)) * be[y].x;
+          const float d1 = exp2f(acs_diff(Gr[r], Lr[r], Gc[y].y, Lc[y].y)) * be[y].y;
           const float x0 = c < rows[r] ? n1[y][2 * r] * d0 * w1[r] : 0.f;
           const float x1 = c + 1 < rows[r] ? n1[y][2 * r + 1] * d1 * w1[r] : 0.f;
           const float z0 = c <= rows[r] ? n2[y][2 * r] * d0 * w2 : 0.f;
@@ -363,11 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
       if (lane == 0) sm.inner[x][warp] = sum;
     }
     uint32_t fx[2], ff[2], fu[2];
+    const float unit = vec[kVecUnit];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const float eg = vec[kVecEg + rows[r]], be = vec[kVecBeta + rows[r]];
-      fx[r] = twice(a.scale * eg);
-      ff[r] = twice(-eg * be);
+      fx[r] = twice(a.scale * eg * unit);
+      ff[r] = twice(-eg * be * unit);
       fu[r] = twice(vec[kVecTail + rows[r]] * be);
     }
     float state[2] = {0.f, 0.f}, down[2] = {0.f, 0.f};

@@ -27,6 +27,7 @@ namespace {
 using namespace mma16;
 
 constexpr int kThreads = 128;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = float(1.4426950408889634 - double(kLog2e));
 constexpr int kPad = kChunk + 4;   // floats of a row of A and X in shared memory
 
 template <int N>
@@ -202,12 +203,14 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
     // running sums of g as hi + lo by a scan over 32 lanes x 2 tokens, warp w < 2 for head w
     if (warp < nh) {
       const int h = grp * s.hpg + h0 + warp;
-      float v[2];
+      float v[2], vl[2];   // g log2(e), and what its rounding left over
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
         // a decay to nothing stays a finite number: exp(-1e4) is zero all the same
-        v[i] = t < n ? fmaxf(a.g[(b + t) * s.H + h], -1e4f) : 0.f;
+        const float g = t < n ? fmaxf(a.g[(b + t) * s.H + h], -1e4f) : 0.f;
+        v[i] = __fmul_rn(g, kLog2e);
+        vl[i] = fmaf(g, kLog2eLow, fmaf(g, kLog2e, -v[i]));
         sm.beta[warp][t] = t < n ? a.beta[(b + t) * s.H + h] : 0.f;
       }
       auto add = [](float &hi, float &lo, float yh, float yl) {   // (hi, lo) += (yh, yl)
@@ -216,8 +219,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
         lo = __fadd_rn(__fadd_rn(lo, yl), err);
         hi = sum;
       };
-      float hi = v[0], lo = 0.f;
-      add(hi, lo, v[1], 0.f);
+      float hi = v[0], lo = vl[0];
+      add(hi, lo, v[1], vl[1]);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const float ph = __shfl_up_sync(~0u, hi, d), pl = __shfl_up_sync(~0u, lo, d);
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
       sm.Gl[warp][2 * lane + 1] = lo;
       float eh = __shfl_up_sync(~0u, hi, 1), el = __shfl_up_sync(~0u, lo, 1);
       if (lane == 0) eh = el = 0.f;
-      add(eh, el, v[0], 0.f);
+      add(eh, el, v[0], vl[0]);
       sm.G[warp][2 * lane] = eh;
       sm.Gl[warp][2 * lane] = el;
     }
@@ -245,8 +248,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int t = rows[i];
-            const float d0 = c <= t ? __expf(acs_diff(Gr[i], Glr[i], g0, l0)) : 0.f;
-            const float d1 = c + 1 <= t ? __expf(acs_diff(Gr[i], Glr[i], g1, l1)) : 0.f;
+            const float d0 = c <= t ? exp2f(acs_diff(Gr[i], Glr[i], g0, l0)) : 0.f;
+            const float d1 = c + 1 <= t ? exp2f(acs_diff(Gr[i], Glr[i], g1, l1)) : 0.f;
             sm.L[w][c][t] = c < t ? d0 * kk[j][2 * i] * (ka * ka) : 0.f;
             sm.L[w][c + 1][t] = c + 1 < t ? d1 * kk[j][2 * i + 1] * (ka * ka) : 0.f;
             *reinterpret_cast<uint32_t *>(P + swz(t, j, 128) + 4 * (lane & 3)) =
@@ -255,8 +258,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
         }
       if (tid < kChunk) {
         float *v = o.vec + at * kVec;
-        v[kVecEg + tid] = expf(G[tid] + Gl[tid]);
-        v[kVecTail + tid] = expf(acs_diff(G[kChunk - 1], Gl[kChunk - 1], G[tid], Gl[tid]));
+        v[kVecEg + tid] = exp2f(G[tid] + Gl[tid]);
+        v[kVecTail + tid] = exp2f(acs_diff(G[kChunk - 1], Gl[kChunk - 1], G[tid], Gl[tid]));
         v[kVecBeta + tid] = sm.beta[w][tid];
         v[kVecG + tid] = G[tid];
         v[kVecGl + tid] = Gl[tid];

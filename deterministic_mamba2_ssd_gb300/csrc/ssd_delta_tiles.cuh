@@ -34,7 +34,8 @@ constexpr int kVecTail = 64;    // exp(G_C - G_t)
 constexpr int kVecBeta = 128;
 constexpr int kVecTau = 192;    // 2^tau_t
 constexpr int kVecKa = 256;     // 2^a
-constexpr int kVecG = 272;      // G_t
+constexpr int kVecUnit = 261;   // S16's scale beside 2^r: 1, after a sequence's first chunk 2^(4+a) of the chunk before (written by the chain)
+constexpr int kVecG = 272;      // G_t log2(e): decays are powers of two, their exponents differences of sums kept in two floats
 constexpr int kVecGl = 336;     // and what its rounding left over
 constexpr int kVec = 400;
 constexpr int kVecChain = 260;  // the part that the chains read
