@@ -542,12 +542,15 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
       }
     }
     first_done<kStrips, kHand>();
-    float2 be[2];
+    float2 be[2], tau[2];
     {
       uint32_t vw[kM][4];
       load_v(vw, c);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) be[i] = vec2(vec + kVecBeta, w, i, lane);
+      for (int i = 0; i < 2; ++i) {
+        be[i] = vec2(vec + kVecBeta, w, i, lane);
+        tau[i] = vec2(vec + kVecTau, w, i, lane);
+      }
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         float B[2][4];
@@ -560,8 +563,8 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
             const float2 v = unpack_bf16(vw[m][2 * i + r]);
             R[m][i][2 * r] = fmaf(-c0, R[m][i][2 * r], v.x * sc.dn);
             R[m][i][2 * r + 1] = fmaf(-c1, R[m][i][2 * r + 1], v.y * sc.dn);
-            B[i][2 * r] = R[m][i][2 * r] * be[i].x;
-            B[i][2 * r + 1] = R[m][i][2 * r + 1] * be[i].y;
+            B[i][2 * r] = R[m][i][2 * r] * (be[i].x * tau[i].x);
+            B[i][2 * r + 1] = R[m][i][2 * r + 1] * (be[i].y * tau[i].y);
           }
         }
         to_a<kTerms>(B[0], B[1], ra);
@@ -600,10 +603,9 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
         for (int m = 0; m < kM; ++m)
 #pragma unroll
           for (int i = 0; i < 8; ++i) E[m][i / 4][i % 4] += E2[m][i / 4][i % 4];
-      float2 tau[2], tl[2];
+      float2 tl[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        tau[i] = vec2(vec + kVecTau, w, i, lane);
         tl[i] = vec2(vec + kVecTail, w, i, lane);
         tl[i].x *= 0.0625f;
         tl[i].y *= 0.0625f;
@@ -838,7 +840,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
       }
     }
     first_done<kStrips, kHand>();
-    float2 be[2], eg[2];
+    float2 be[2], eg[2], tau[2];
     {
       float A[kM][2][4] = {};
 #pragma unroll
@@ -852,11 +854,11 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
       float2 tl[2], bt[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 tau = vec2(vec + kVecTau, w, i, lane);
+        tau[i] = vec2(vec + kVecTau, w, i, lane);
         eg[i] = vec2(vec + kVecEg, w, i, lane);
         tl[i] = vec2(vec + kVecTail, w, i, lane);
         be[i] = vec2(vec + kVecBeta, w, i, lane);
-        bt[i] = make_float2(be[i].x * tau.x, be[i].y * tau.y);
+        bt[i] = make_float2(be[i].x * tau[i].x, be[i].y * tau[i].y);
       }
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
@@ -897,8 +899,8 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
 #pragma unroll
           for (int r = 0; r < 4; r += 2) {
             const float2 xv = unpack(x[2 * i + r / 2]);
-            F[m][i][r] -= C[m][i][r];
-            F[m][i][r + 1] -= C[m][i][r + 1];
+            F[m][i][r] = fmaf(-tau[i].x, C[m][i][r], F[m][i][r]);
+            F[m][i][r + 1] = fmaf(-tau[i].y, C[m][i][r + 1], F[m][i][r + 1]);
             W[i][r] = F[m][i][r] * (be[i].x * c0);
             W[i][r + 1] = F[m][i][r + 1] * (be[i].y * c1);
             Z[i][r] = xv.x * eg[i].x;

@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_tile_kernel(Shape s, Args a
         wcol[2 * y] = wcol[2 * y + 1] = 0.f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float d0 = exp2f(acs_diff(Gr[r], Lr[r], Gc[y].x, Lc[y].x)) * be[y].x;
-          const float d1 = exp2f(acs_diff(Gr[r], Lr[r], Gc[y].y, Lc[y].y)) * be[y].y;
+          const float d0 = pow2(acs_diff(Gr[r], Lr[r], Gc[y].x, Lc[y].x)) * be[y].x;
+          const float d1 = pow2(acs_diff(Gr[r], Lr[r], Gc[y].y, Lc[y].y)) * be[y].y;
           const float x0 = c < rows[r] ? n1[y][2 * r] * d0 * w1[r] : 0.f;
           const float x1 = c + 1 < rows[r] ? n1[y][2 * r + 1] * d1 * w1[r] : 0.f;
           const float z0 = c <= rows[r] ? n2[y][2 * r] * d0 * w2 : 0.f;

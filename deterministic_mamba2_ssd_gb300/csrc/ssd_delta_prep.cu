@@ -6,15 +6,23 @@
 //     (I + L diag(beta))^-1 R = R - Y (beta R),
 //     (I + diag(beta) L)^-T U = U - Y^T (beta U).
 //
-// CTA (chunk slot, group): k and q of the chunk once, K K^T and Q K^T on the
-// tensor cores (fp16 operands are exact here: bf16 rows scaled by a power of
-// two), then the heads of the group, two at a time.  Y is found in fp32 by
-// forward substitution, one thread a column, 16 rows at a time:
-//     Y[t][j] = L[t][j] - sum_{j<s<t} L[t][s] beta_s Y[s][j],
-// the 16 rows as packed pairs of fp32, earlier rows of the column read back
-// from shared memory.  (With the whole column in registers the unrolled code,
-// 2000 products, did not fit the instruction cache: 220 us instead of 80 for
-// 256 chunks of 32 heads.)
+// CTA (chunk slot, group), four warps: k and q of the chunk once, K K^T and
+// Q K^T on the tensor cores (fp16 operands are exact here: bf16 rows scaled by
+// a power of two), then the heads of the group.  With powers of two r_t above
+// |k_t|, L = r L' r with |L'| < 1, Y = r Y' r, and Y' = (I + L' c)^-1 L' with
+// c = beta r^2.  In blocks of 16 tokens, T_I the inverse of I + (L' c)_II:
+//     Y'_I = T_I (L'_I - sum_{J<I} L'_IJ (c Y'_J)).
+// The diagonal blocks are inverted in fp32, a column a lane.  The rest are
+// products of 16 x 16 blocks in two fp16 terms (22 bits): a warp has a column
+// block, transposed, so that each step's accumulators are the next one's left
+// operand and Y' never leaves the registers before it is done.
+//
+// What bounds it is instructions and their latency (half of the issue slots
+// are taken, 16 warps an SM): the 64 x 64 elements of a head cost 170 us for
+// 256 chunks of 64 heads in 8 groups, 132 us for 256 chunks of 32 heads in 16,
+// where the group's own part weighs more.  Forward substitution in fp32, one
+// thread a column, took 250 and 171: its longest columns all lay on two of the
+// four schedulers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +36,9 @@ using namespace mma16;
 
 constexpr int kThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = float(1.4426950408889634 - double(kLog2e));
-constexpr int kPad = kChunk + 4;   // floats of a row of A and X in shared memory
+constexpr int kTile = kChunk * 128;   // bytes of a 64 x 64 tile of fp16
+constexpr int kTRow = 48;             // bytes of a row of a 16 x 16 inverse: eight rows fall into different banks
+constexpr int kScan = kThreads / 32;  // heads whose sums of g are taken at a time
 
 template <int N>
 struct Smem {
@@ -36,13 +46,16 @@ struct Smem {
     struct {
       __half k[kChunk * N], q[kChunk * N];
     };
-    struct {   // of two heads, once the products of k and q are taken
-      float L[2][kChunk][kPad];   // [s][t]
-      float Y[2][kChunk][kPad];   // [t][s]
+    struct {   // of a head, once the products of k and q are taken
+      uint8_t L[2][kTile];               // L' in two terms, [t][s]
+      uint8_t Y[2][kTile];               // Y' scaled, in two terms, [t][s]
+      uint8_t T[2][4][16 * kTRow];       // inverses of the diagonal blocks, in two terms
+      float A[4][16][20];                // the diagonal blocks of A'
     };
   };
   float top[2][kThreads / 32];    // largest |k|, |q| of each warp's part
-  float G[2][kChunk], Gl[2][kChunk], beta[2][kChunk];
+  float r[kChunk];                // powers of two above |k16_t|
+  float G[kScan][kChunk], Gl[kScan][kChunk], beta[kScan][kChunk];
 };
 
 // This thread's part of the chunk's rows of q or k (16-byte pieces; rows past the end zero) and its largest magnitude.
@@ -102,54 +115,29 @@ __device__ __forceinline__ void rows_out(const uint4 (&raw)[kChunk * N / 8 / kTh
   }
 }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b),
-                     z = *reinterpret_cast<unsigned long long *>(&c);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(z) : "l"(x), "l"(y));
-  return *reinterpret_cast<float2 *>(&z);
+// Products of a 16 x 16 left operand and a right operand, both in two terms: 22 bits.
+__device__ __forceinline__ void mul3(float (&d)[2][4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                     const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+  mma(d[0], ah, bh[0], bh[1]);
+  mma(d[1], ah, bh[2], bh[3]);
+  mma(d[0], al, bh[0], bh[1]);
+  mma(d[1], al, bh[2], bh[3]);
+  mma(d[0], ah, bl[0], bl[1]);
+  mma(d[1], ah, bl[2], bl[3]);
 }
-
-// Column j of Y; a warp has 32 neighbouring columns, the first of them j0 (rows up to j0 are zero).
-__device__ __forceinline__ void solve(const float (*L)[kPad], const float *beta, float (*Y)[kPad], int j, int j0) {
-#pragma unroll 1
-  for (int r0 = j0; r0 < kChunk; r0 += 16) {
-    float2 acc[8];
-    const bool below = r0 + 16 > j;   // this strip of rows has a part of L's column j
+// 16 x 16 accumulators as a left operand in two terms.
+__device__ __forceinline__ void to_left(const float (&d)[2][4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float4 v = below ? *reinterpret_cast<const float4 *>(&L[j][r0 + 2 * i]) : make_float4(0.f, 0.f, 0.f, 0.f);
-      acc[i] = make_float2(v.x, v.y);
-      acc[i + 1] = make_float2(v.z, v.w);
-    }
-#pragma unroll 4
-    for (int s = j0; s < r0; ++s) {
-      const float z = -beta[s] * Y[s][j];
-      const float2 zz = make_float2(z, z);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float4 v = *reinterpret_cast<const float4 *>(&L[s][r0 + 2 * i]);
-        acc[i] = fma2(make_float2(v.x, v.y), zz, acc[i]);
-        acc[i + 1] = fma2(make_float2(v.z, v.w), zz, acc[i + 1]);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const float y = t & 1 ? acc[t >> 1].y : acc[t >> 1].x;
-      Y[r0 + t][j] = y;
-      const float z = -beta[r0 + t] * y;
-      const float2 zz = make_float2(z, z);
-#pragma unroll
-      for (int i = (t + 1) / 4 * 2; i < 8; i += 2) {   // L is zero on and above the diagonal of this block
-        const float4 v = *reinterpret_cast<const float4 *>(&L[r0 + t][r0 + 2 * i]);
-        acc[i] = fma2(make_float2(v.x, v.y), zz, acc[i]);
-        acc[i + 1] = fma2(make_float2(v.z, v.w), zz, acc[i + 1]);
-      }
-    }
+  for (int i = 0; i < 4; ++i) {
+    uint32_t p[2];
+    split<2>(d[i >> 1][2 * (i & 1)], d[i >> 1][2 * (i & 1) + 1], p);
+    hi[i] = p[0];
+    lo[i] = p[1];
   }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o, int two_planes, int vec) {
+__global__ void __launch_bounds__(kThreads, 4) prep_kernel(Shape s, Args a, Tiles o, int two_planes, int vec) {
   extern __shared__ __align__(128) uint8_t raw[];
   Smem<N> &sm = *reinterpret_cast<Smem<N> *>(raw);
   const int64_t slot = blockIdx.x;
@@ -177,130 +165,240 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Shape s, Args a, Tiles o
   rows_out<N>(rk, pow2_inv(ka), sm.k, o.K16 + tile);
   rows_out<N>(rq, pow2_inv(ka), sm.q, o.Q16 + tile);
   __syncthreads();
-  // rows 16 warp.. of K K^T and Q K^T, columns up to the diagonal block
-  float kk[8][4] = {}, qk[8][4] = {};
-  const uint32_t ks = smem_at(sm.k), qs = smem_at(sm.q);
+  // K K^T and Q K^T: ten blocks of 16 x 16 up to the diagonal and the two above it that readers of P16 touch, three a warp
+  const int bt[3] = {warp == 0 ? 0 : warp == 1 ? 2 : 3, warp == 0 ? 1 : warp == 1 ? 2 : 3, (0x2021 >> (4 * warp)) & 3};
+  const int bs[3] = {warp == 3 ? 2 : 0, (0x3110 >> (4 * warp)) & 3, (0x3121 >> (4 * warp)) & 3};
+  float kk[3][2][4] = {}, qk[3][2][4] = {};
+  {
+    const uint32_t ks = smem_at(sm.k), qs = smem_at(sm.q);
+#pragma unroll 2
+    for (int k0 = 0; k0 < N; k0 += 16)
 #pragma unroll
-  for (int k0 = 0; k0 < N; k0 += 16) {
-    uint32_t ak[4], aq[4];
-    ldsm4(ak, a_addr(ks, 16 * warp, k0, 2 * N, lane));
-    ldsm4(aq, a_addr(qs, 16 * warp, k0, 2 * N, lane));
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= warp) {
-        uint32_t bb[4];
-        ldsm4(bb, b_addr(ks, 16 * j, k0, 2 * N, lane));
-        mma(kk[2 * j], ak, bb[0], bb[1]);
-        mma(kk[2 * j + 1], ak, bb[2], bb[3]);
-        mma(qk[2 * j], aq, bb[0], bb[1]);
-        mma(qk[2 * j + 1], aq, bb[2], bb[3]);
+      for (int i = 0; i < 3; ++i) {
+        uint32_t ak[4], aq[4], bb[4];
+        ldsm4(ak, a_addr(ks, 16 * bt[i], k0, 2 * N, lane));
+        ldsm4(aq, a_addr(qs, 16 * bt[i], k0, 2 * N, lane));
+        ldsm4(bb, b_addr(ks, 16 * bs[i], k0, 2 * N, lane));
+        mma(kk[i][0], ak, bb[0], bb[1]);
+        mma(kk[i][1], ak, bb[2], bb[3]);
+        mma(qk[i][0], aq, bb[0], bb[1]);
+        mma(qk[i][1], aq, bb[2], bb[3]);
       }
   }
-  const int rows[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};
-  for (int h0 = 0; h0 < s.hpg; h0 += 2) {
-    const int nh = min(2, s.hpg - h0);
-    __syncthreads();   // the products of k and q are taken, the heads before are done with L, Y and the vectors
-    // running sums of g as hi + lo by a scan over 32 lanes x 2 tokens, warp w < 2 for head w
-    if (warp < nh) {
-      const int h = grp * s.hpg + h0 + warp;
-      float v[2], vl[2];   // g log2(e), and what its rounding left over
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+  // r_t from the diagonals: |k16_t k16_s| < r_t r_s
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        // a decay to nothing stays a finite number: exp(-1e4) is zero all the same
-        const float g = t < n ? fmaxf(a.g[(b + t) * s.H + h], -1e4f) : 0.f;
-        v[i] = __fmul_rn(g, kLog2e);
-        vl[i] = fmaf(g, kLog2eLow, fmaf(g, kLog2e, -v[i]));
-        sm.beta[warp][t] = t < n ? a.beta[(b + t) * s.H + h] : 0.f;
-      }
-      auto add = [](float &hi, float &lo, float yh, float yl) {   // (hi, lo) += (yh, yl)
-        const float sum = __fadd_rn(hi, yh), bb = __fsub_rn(sum, hi);
-        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, bb)), __fsub_rn(yh, bb));
-        lo = __fadd_rn(__fadd_rn(lo, yl), err);
-        hi = sum;
+  for (int i = 0; i < 3; ++i)
+    if (bt[i] == bs[i] && (lane & 3) == (g >> 1)) {
+      const float lo = g & 1 ? kk[i][0][1] : kk[i][0][0], hi = g & 1 ? kk[i][1][3] : kk[i][1][2];
+      auto root = [](float x) {   // of x < 2^e, 2^ceil(e/2)
+        if (!(x > 0.f)) return 1.f;
+        const int e = int(__float_as_uint(x) >> 23) - 126;
+        return __uint_as_float(uint32_t(((e + 1) >> 1) + 127) << 23);
       };
-      float hi = v[0], lo = vl[0];
-      add(hi, lo, v[1], vl[1]);
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const float ph = __shfl_up_sync(~0u, hi, d), pl = __shfl_up_sync(~0u, lo, d);
-        if (lane >= d) add(hi, lo, ph, pl);
-      }
-      sm.G[warp][2 * lane + 1] = hi;
-      sm.Gl[warp][2 * lane + 1] = lo;
-      float eh = __shfl_up_sync(~0u, hi, 1), el = __shfl_up_sync(~0u, lo, 1);
-      if (lane == 0) eh = el = 0.f;
-      add(eh, el, v[0], vl[0]);
-      sm.G[warp][2 * lane] = eh;
-      sm.Gl[warp][2 * lane] = el;
+      sm.r[16 * bt[i] + g] = root(lo);
+      sm.r[16 * bt[i] + g + 8] = root(hi);
     }
-    __syncthreads();
-    for (int w = 0; w < nh; ++w) {
-      const int64_t at = slot * s.H + grp * s.hpg + h0 + w;
-      const float *G = sm.G[w], *Gl = sm.Gl[w];
-      uint8_t *P = reinterpret_cast<uint8_t *>(o.P16 + at * kTri);
-      const float Gr[2] = {G[rows[0]], G[rows[1]]}, Glr[2] = {Gl[rows[0]], Gl[rows[1]]};
+  __syncthreads();   // k and q are done with
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j <= 2 * (warp | 1) + 1) {   // of the blocks above the diagonal, two are read
-          const int c = 8 * j + 2 * (lane & 3);
-          const float g0 = G[c], g1 = G[c + 1], l0 = Gl[c], l1 = Gl[c + 1];
+  for (int i = 0; i < 3; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = rows[i];
-            const float d0 = c <= t ? exp2f(acs_diff(Gr[i], Glr[i], g0, l0)) : 0.f;
-            const float d1 = c + 1 <= t ? exp2f(acs_diff(Gr[i], Glr[i], g1, l1)) : 0.f;
-            sm.L[w][c][t] = c < t ? d0 * kk[j][2 * i] * (ka * ka) : 0.f;
-            sm.L[w][c + 1][t] = c + 1 < t ? d1 * kk[j][2 * i + 1] * (ka * ka) : 0.f;
-            *reinterpret_cast<uint32_t *>(P + swz(t, j, 128) + 4 * (lane & 3)) =
-                pack(d0 * qk[j][2 * i], d1 * qk[j][2 * i + 1]);
+    for (int y = 0; y < 2; ++y) {
+      const float2 rs = *reinterpret_cast<const float2 *>(&sm.r[16 * bs[i] + 8 * y + c2]);
+      const float ra = pow2_inv(sm.r[16 * bt[i] + g]), rb = pow2_inv(sm.r[16 * bt[i] + g + 8]);
+      const float ia = pow2_inv(rs.x), ib = pow2_inv(rs.y);
+      kk[i][y][0] *= ra * ia;
+      kk[i][y][1] *= ra * ib;
+      kk[i][y][2] *= rb * ia;
+      kk[i][y][3] *= rb * ib;
+    }
+  for (int x = tid; x < 2 * kTile / 16; x += kThreads) reinterpret_cast<uint4 *>(sm.Y[0])[x] = make_uint4(0, 0, 0, 0);
+  const uint32_t Ls = smem_at(sm.L[0]), Ys = smem_at(sm.Y[0]), Ts = smem_at(sm.T[0][0]);
+  const uint32_t trow = ((lane & 7) + ((lane >> 4) << 3)) * kTRow + ((lane >> 3) & 1) * 16;
+  for (int i = 0; i < s.hpg; ++i) {
+    if (i % kScan == 0) {
+      // running sums of g log2(e) as hi + lo by a scan over 32 lanes x 2 tokens, a warp a head
+      if (i + warp < s.hpg) {
+        const int h = grp * s.hpg + i + warp;
+        float v[2], vl[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int t = 2 * lane + y;
+          // a decay to nothing stays a finite number: exp(-1e4) is zero all the same
+          const float x = t < n ? fmaxf(a.g[(b + t) * s.H + h], -1e4f) : 0.f;
+          v[y] = __fmul_rn(x, kLog2e);
+          vl[y] = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -v[y]));
+          sm.beta[warp][t] = t < n ? a.beta[(b + t) * s.H + h] : 0.f;
+        }
+        auto add = [](float &hi, float &lo, float yh, float yl) {   // (hi, lo) += (yh, yl)
+          const float sum = __fadd_rn(hi, yh), bb = __fsub_rn(sum, hi);
+          const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, bb)), __fsub_rn(yh, bb));
+          lo = __fadd_rn(__fadd_rn(lo, yl), err);
+          hi = sum;
+        };
+        float hi = v[0], lo = vl[0];
+        add(hi, lo, v[1], vl[1]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float ph = __shfl_up_sync(~0u, hi, d), pl = __shfl_up_sync(~0u, lo, d);
+          if (lane >= d) add(hi, lo, ph, pl);
+        }
+        sm.G[warp][2 * lane + 1] = hi;
+        sm.Gl[warp][2 * lane + 1] = lo;
+        float eh = __shfl_up_sync(~0u, hi, 1), el = __shfl_up_sync(~0u, lo, 1);
+        if (lane == 0) eh = el = 0.f;
+        add(eh, el, v[0], vl[0]);
+        sm.G[warp][2 * lane] = eh;
+        sm.Gl[warp][2 * lane] = el;
+      }
+      __syncthreads();
+    }
+    const int64_t at = slot * s.H + grp * s.hpg + i;
+    const float *G = sm.G[i % kScan], *Gl = sm.Gl[i % kScan], *beta = sm.beta[i % kScan];
+    uint8_t *P = reinterpret_cast<uint8_t *>(o.P16 + at * kTri);
+    // L' and the decayed scores
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      const bool mine = bt[x] >= bs[x], diag = bt[x] == bs[x];
+      const int t0 = 16 * bt[x] + g;
+      const float Gr[2] = {G[t0], G[t0 + 8]}, Lr[2] = {Gl[t0], Gl[t0 + 8]};
+      float l[2][2][2], p[2][2][2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int c = 16 * bs[x] + 8 * y + c2;
+        const float2 gc = *reinterpret_cast<const float2 *>(&G[c]), lc = *reinterpret_cast<const float2 *>(&Gl[c]);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int t = t0 + 8 * r;
+          const float d0 = c <= t ? pow2(acs_diff(Gr[r], Lr[r], gc.x, lc.x)) : 0.f;
+          const float d1 = c + 1 <= t ? pow2(acs_diff(Gr[r], Lr[r], gc.y, lc.y)) : 0.f;
+          p[y][r][0] = d0 * qk[x][y][2 * r];
+          p[y][r][1] = d1 * qk[x][y][2 * r + 1];
+          l[y][r][0] = c < t ? d0 * kk[x][y][2 * r] : 0.f;
+          l[y][r][1] = c + 1 < t ? d1 * kk[x][y][2 * r + 1] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t to = swz(t0 + 8 * r, 2 * bs[x] + y, 128) + 2 * c2;
+          *reinterpret_cast<uint32_t *>(P + to) = pack(p[y][r][0], p[y][r][1]);
+          if (mine) {
+            uint32_t w[2];
+            split<2>(l[y][r][0], l[y][r][1], w);
+            *reinterpret_cast<uint32_t *>(sm.L[0] + to) = w[0];
+            *reinterpret_cast<uint32_t *>(sm.L[1] + to) = w[1];
+          }
+          if (diag) {
+            const int c = 16 * bs[x] + 8 * y + c2;
+            const float2 rs = *reinterpret_cast<const float2 *>(&sm.r[c]), be = *reinterpret_cast<const float2 *>(&beta[c]);
+            *reinterpret_cast<float2 *>(&sm.A[bt[x]][g + 8 * r][8 * y + c2]) =
+                make_float2(l[y][r][0] * (be.x * (rs.x * ka) * (rs.x * ka)), l[y][r][1] * (be.y * (rs.y * ka) * (rs.y * ka)));
           }
         }
-      if (tid < kChunk) {
-        float *v = o.vec + at * kVec;
-        v[kVecEg + tid] = exp2f(G[tid] + Gl[tid]);
-        v[kVecTail + tid] = exp2f(acs_diff(G[kChunk - 1], Gl[kChunk - 1], G[tid], Gl[tid]));
-        v[kVecBeta + tid] = sm.beta[w][tid];
-        v[kVecG + tid] = G[tid];
-        v[kVecGl + tid] = Gl[tid];
-        if (tid == 0) v[kVecKa] = ka;
-      }
+    }
+    if (tid < kChunk) {
+      float *v = o.vec + at * kVec;
+      v[kVecEg + tid] = pow2(G[tid] + Gl[tid]);
+      v[kVecTail + tid] = pow2(acs_diff(G[kChunk - 1], Gl[kChunk - 1], G[tid], Gl[tid]));
+      v[kVecBeta + tid] = beta[tid];
+      v[kVecTau + tid] = ka * sm.r[tid];
+      v[kVecG + tid] = G[tid];
+      v[kVecGl + tid] = Gl[tid];
+      if (tid == 0) v[kVecKa] = ka;
     }
     __syncthreads();
-    if ((warp >> 1) < nh) solve(sm.L[warp >> 1], sm.beta[warp >> 1], sm.Y[warp >> 1], tid & 63, 32 * (warp & 1));
-    __syncthreads();
-    // rows of Y to fp16, eight lanes a row
-    for (int w = 0; w < nh; ++w) {
-      const int64_t at = slot * s.H + grp * s.hpg + h0 + w;
-      uint8_t *Y = reinterpret_cast<uint8_t *>(o.Y16 + at * 2 * kTri);
-#pragma unroll 2
-      for (int r = tid / 8; r < kChunk; r += kThreads / 8) {
-        const int l = tid % 8;
-        // columns from 32 have no rows above 32
-        const bool on = l < 4 || r >= 32;
-        const float4 u0 = on ? *reinterpret_cast<const float4 *>(&sm.Y[w][r][8 * l]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 u1 = on ? *reinterpret_cast<const float4 *>(&sm.Y[w][r][8 * l + 4]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-        float m = 0.f;
+    {
+      // column lane % 16 of the inverse of diagonal block `warp`
+      const int j = lane & 15;
+      float T[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+      for (int t = 0; t < 16; ++t) {
+        float x[2] = {t == j ? 1.f : 0.f, 0.f};
 #pragma unroll
-        for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        const float sc = pow2_above(m), inv = pow2_inv(sc);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t p[2];
-          split<2>(v[2 * i] * inv, v[2 * i + 1] * inv, p);
-          hi[i] = p[0];
-          lo[i] = p[1];
+        for (int z = 0; z < t; z += 4) {
+          const float4 w = *reinterpret_cast<const float4 *>(&sm.A[warp][t][z]);
+          x[0] = fmaf(-w.x, T[z], x[0]);
+          if (z + 1 < t) x[1] = fmaf(-w.y, T[z + 1], x[1]);
+          if (z + 2 < t) x[0] = fmaf(-w.z, T[z + 2], x[0]);
+          if (z + 3 < t) x[1] = fmaf(-w.w, T[z + 3], x[1]);
         }
-        *reinterpret_cast<uint4 *>(Y + swz(r, l, 128)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (two_planes)
-          *reinterpret_cast<uint4 *>(Y + 2 * kTri + swz(r, l, 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (l == 0) o.vec[at * kVec + kVecTau + r] = sc;
+        T[t] = x[0] + x[1];
+      }
+      // the two halves of the warp store a term each
+      uint8_t *to = sm.T[lane >> 4][warp] + 2 * j;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        const __half hi = __float2half_rn(T[t]);
+        *reinterpret_cast<__half *>(to + t * kTRow) = lane >> 4 ? __float2half_rn(T[t] - __half2float(hi)) : hi;
       }
     }
+    __syncthreads();
+    // column block `warp` of Y'^T, row by row of blocks: (L'^T - sum_J (c Y'_J)^T L'_IJ^T) T_II^T
+    float y[4][2][4];
+    {
+      uint32_t uh[3][4], ul[3][4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int I = warp + d;
+        if (I >= 4) break;
+        float v[2][4];
+        {
+          uint32_t wh[4], wl[4];
+          ldsm4t(wh, b_addr(Ls, 16 * I, 16 * warp, 128, lane));
+          ldsm4t(wl, b_addr(Ls + kTile, 16 * I, 16 * warp, 128, lane));
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float2 fh = unpack(wh[z]), fl = unpack(wl[z]);
+            v[z >> 1][2 * (z & 1)] = fh.x + fl.x;
+            v[z >> 1][2 * (z & 1) + 1] = fh.y + fl.y;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < d; ++e) {
+          uint32_t wh[4], wl[4];
+          ldsm4(wh, b_addr(Ls, 16 * I, 16 * (warp + e), 128, lane));
+          ldsm4(wl, b_addr(Ls + kTile, 16 * I, 16 * (warp + e), 128, lane));
+          mul3(v, uh[e], ul[e], wh, wl);
+        }
+        uint32_t vh[4], vl[4], th[4], tl[4];
+        to_left(v, vh, vl);
+        ldsm4(th, Ts + I * 16 * kTRow + trow);
+        ldsm4(tl, Ts + (4 + I) * 16 * kTRow + trow);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) y[d][z >> 2][z & 3] = 0.f;
+        mul3(y[d], vh, vl, th, tl);
+        if (d < 3) {
+          float u[2][4];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int c = 16 * I + 8 * z + c2;
+            const float2 rs = *reinterpret_cast<const float2 *>(&sm.r[c]), be = *reinterpret_cast<const float2 *>(&beta[c]);
+            const float f0 = -be.x * (rs.x * ka) * (rs.x * ka), f1 = -be.y * (rs.y * ka) * (rs.y * ka);
+            u[z][0] = y[d][z][0] * f0;
+            u[z][1] = y[d][z][1] * f1;
+            u[z][2] = y[d][z][2] * f0;
+            u[z][3] = y[d][z][3] * f1;
+          }
+          to_left(u, uh[d], ul[d]);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int I = warp + d;
+      if (I >= 4) break;
+      uint32_t wh[4], wl[4];
+      to_left(y[d], wh, wl);
+      stsm4t(b_addr(Ys, 16 * I, 16 * warp, 128, lane), wh);
+      stsm4t(b_addr(Ys + kTile, 16 * I, 16 * warp, 128, lane), wl);
+    }
+    __syncthreads();
+    uint8_t *Y = reinterpret_cast<uint8_t *>(o.Y16 + at * 2 * kTri);
+#pragma unroll 4
+    for (int x = tid; x < (two_planes ? 2 : 1) * kTile / 16; x += kThreads)
+      reinterpret_cast<uint4 *>(Y)[x] = reinterpret_cast<const uint4 *>(sm.Y[0])[x];
   }
 }
 

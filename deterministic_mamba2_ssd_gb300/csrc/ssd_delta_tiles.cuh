@@ -8,7 +8,8 @@
 //                            so that bf16 input is exact down to 2^-21 of it
 //                            and no sum of 128 products leaves fp16's range
 //   Y16 (slot, head):        (I + L diag(beta))^-1 L, rows [t][s] times
-//                            2^-tau_t; a second plane with the rounding left over
+//                            2^-(tau_t + tau_s); a second plane with the rounding
+//                            left over
 //   P16 (slot, head):        exp(G_t - G_s) (q16_t . k16_s), s <= t
 //                            (zero above the diagonal; there, only the 16 x 16
 //                            blocks (0, 1) and (2, 3) are written)
@@ -32,7 +33,7 @@ namespace delta {
 constexpr int kVecEg = 0;       // exp(G_t)
 constexpr int kVecTail = 64;    // exp(G_C - G_t)
 constexpr int kVecBeta = 128;
-constexpr int kVecTau = 192;    // 2^tau_t
+constexpr int kVecTau = 192;    // 2^tau_t, above |k_t|
 constexpr int kVecKa = 256;     // 2^a
 constexpr int kVecUnit = 261;   // S16's scale beside 2^r: 1, after a sequence's first chunk 2^(4+a) of the chunk before (written by the chain)
 constexpr int kVecG = 272;      // G_t log2(e): decays are powers of two, their exponents differences of sums kept in two floats
@@ -79,6 +80,12 @@ inline BwdTiles carve_bwd_tiles(const Shape &s, void *p) {
   t.ub = c.take<float>(s.slots * s.H * s.P / 16);
   t.bytes = c.bytes();
   return t;
+}
+
+__device__ __forceinline__ float pow2(float x) {   // to 2^-22; zero below 2^-126
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Kernel launches (ssd_delta_prep.cu, ssd_delta_chain.cu, ssd_delta_grads.cu).
