@@ -404,14 +404,16 @@ class DeltaFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, beta, scale, init_states, cu_seqlens):
         o, final, saved = _delta_run(q, k, v, g, beta, scale, cu_seqlens, init_states, True, True, None)
-        ctx.saved = saved
         saved.tensors["final"] = None
+        ctx.names = tuple(saved.tensors)
+        ctx.save_for_backward(*saved.tensors.values())
+        ctx.plan, ctx.scale = saved.plan, saved.scale
         ctx.set_materialize_grads(False)
         return o, final
 
     @staticmethod
     def backward(ctx, do, dfinal):
-        s = ctx.saved
+        s = DeltaSaved(ctx.plan, dict(zip(ctx.names, ctx.saved_tensors)), ctx.scale)
         q, d = s.tensors["q"], s.dims
         if do is None:
             do = torch.zeros(tuple(q.shape[:2]) + (d.nheads, d.headdim), dtype=q.dtype, device=q.device)

@@ -1,36 +1,45 @@
 // ssd_delta_chain.cu -- the gated delta rule from chunk to chunk: the forward
 // recurrence of S with the outputs, and the reverse recurrence of dS.
 //
-// Rows of S (one for each element of v) never mix.  A strip of 16 rows, the
-// height of a warp-level product, goes through the whole sequence with four
-// warps; its S stays in their registers as fp32 accumulators, dstate / 4
-// columns a warp.  Every product of a chunk has the strip's rows on its left
-// and tiles of the chunk (K, Q, Y, P; see ssd_delta_tiles.cuh) on its right:
+// Rows of S (one for each element of v) never mix.  A strip of 32 rows goes
+// through the whole sequence with four warps; its S stays in their registers
+// as fp32 accumulators, dstate / 4 columns a warp.  Every product of a chunk
+// has the strip's rows on its left and tiles of the chunk (K, Q, Y, P; see
+// ssd_delta_tiles.cuh) on its right; S = u S' with u = 2^(4+a) of the chunk
+// before (1 at first), r_t the powers of two above |k_t|:
 //
-//   forward    X = S K16^T                    (p x t)   R = V - exp(G) 2^a X
-//              E = R - (beta R) Y16^T 2^tau   (p x t)   U = beta 2^a E
-//              O = (exp(G) S Q16^T + U P16^T) scale 2^a
-//              S = exp(G_C) S + (U exp(G_C - G)) K16
+//   forward    R = V - exp(G) u 2^a S' K16^T                         (p x t)
+//              E = R - r (beta r R) Y16^T,   U = beta E
+//              O = scale 2^2a (exp(G) (u / 2^a) S' Q16^T + U P16^T)
+//              S' = exp(G_C) (u / 2^(4+a)) S' + (2^-4 U exp(G_C - G)) K16
 //   backward   dU = (exp(G_C - G) dS K16^T + scale 2^a dO P16) 2^a
-//              F = dU - (beta 2^tau dU) Y16,            dv = beta F
+//              F = dU - r (beta r dU) Y16,              dv = beta F
 //              dS = exp(G_C) dS + scale 2^a (exp(G) dO) Q16 - (exp(G) 2^a dv) K16
 //
-// Each warp has 16 of the chunk's tokens as columns of X, R, E, O (dU, F) and
-// a quarter of dstate as columns of S, so the left operands S, R and U pass
-// through shared memory (16 rows, 2 to 4 KB) with one barrier each: three
-// barriers a chunk.  What bounds the kernel is the latency of that chain, not
-// a rate: few heads leave few strips, and every strip is sequential.  Hence
-// the smallest left operand, S in registers, and all work that the next chunk
-// does not wait for (outputs, records) behind the chain's own steps.  One warp
-// a strip, with everything in registers and no barrier, took 3.2 us a chunk
-// (2000 instructions of one warp).
+// Each warp has two tiles of 8 tokens as columns of R, E, O (dU, F) and a
+// quarter of dstate as columns of S, so the left operands S, R and U pass
+// through shared memory with one barrier each: three barriers a chunk.  Copies
+// are the work of four warps of their own.
+//
+// What bounds the kernel is the latency of that chain: few heads leave few
+// strips, and every strip is sequential.  A chunk with two terms (16384 tokens
+// x 32 heads, 128 strips, one a CTA and a warp on each scheduler) takes 2.0 us,
+// some 4100 cycles, of which the tensor cores are busy 1700 (m16n8k16 every 8
+// cycles): S K and S Q 1250, the two terms of R, U and S 1100, Y 500, the
+// update of S 740.  Measured on the way there: strips of 16 rows 2.3 us (each
+// right operand read from shared memory for one product instead of two, and the
+// reads are what then bounds it); copies issued by the chain's own warps 0.4 us
+// more; one warp a strip, everything in registers, no barrier, 3.2 us; strips
+// of a whole head on tcgen05, 3.5 us (every step waits for the accumulators to
+// come back from tensor memory through four warps on each scheduler).
 //
 // Operands are fp16 with power-of-two scales: the K, Q and Y tiles carry
 // theirs (exact for bf16 k and q), the strip's S, V, dO and all between share
 // one running scale, moved only when the largest value leaves [2^-2, 2^6].
 // One fp16 term is 11 bits (2^-12): enough for what leaves as bf16.  Where the
 // fp32 state itself is asked for, S, R, U and Y are carried as two terms (22
-// bits); k and q are exact either way, and the sums are fp32.
+// bits); k and q are exact either way, and the sums are fp32.  Final states
+// differ from fp64 by 1 to 2e-7 of their size.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -444,7 +453,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
   seq_range(s, a.cu, seq, t0, te);
   const int64_t slot0 = first_slot(s, a.cu, seq, t0), nc = (te - t0 + kChunk - 1) / kChunk;
   auto chunk = [&](int64_t c) {
-    return Chunk{slot0 + c, t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
+    return Chunk{min(slot0 + c, s.slots - 1), t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
   };
   __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
   if (strip == kStrips) {
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_fwd_kernel(
       for (int y = 0; y < kStrips; ++y) {
         const int p = (blockIdx.x * kStrips + y) * kRows, rows = s.P - p;
         const uint8_t *own = smem + L::kOwn + y * L::kStrip;
-        if (c < nc) copy_state<N>(own + L::kS, t.S16 + (((slot0 + c) * s.H + h) * s.P + p) * N, rows);
+        if (c < nc) copy_state<N>(own + L::kS, t.S16 + ((chunk(c).slot * s.H + h) * s.P + p) * N, rows);
         if (c == 0) continue;
         const Chunk ck = chunk(c - 1);
 #pragma unroll
@@ -740,7 +749,7 @@ __global__ void __launch_bounds__(128 * kStrips + kLoaders, 1) chain_bwd_kernel(
   // step i of the sweep takes chunk nc - 1 - i of the sequence
   auto chunk = [&](int64_t i) {
     const int64_t c = nc - 1 - i;
-    return Chunk{slot0 + c, t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
+    return Chunk{min(slot0 + c, s.slots - 1), t0 + c * kChunk, int(min(int64_t(kChunk), te - t0 - c * kChunk))};
   };
   __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv);
   if (strip == kStrips) {

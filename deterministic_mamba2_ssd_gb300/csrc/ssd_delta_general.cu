@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(kGThreads) grads_kernel(Shape s, Args a, const
     if (tid == 0) {   // running sums of g as hi + lo; a decay to nothing stays finite
       float hi = 0.f, lo = 0.f;
       for (int t = 0; t < kChunk; ++t) {
-        const float x = t < n ? fmaxf(a.g[(b + t) * s.H + h], -1e4f) : 0.f;
+        float x = t < n ? a.g[(b + t) * s.H + h] : 0.f;
+        if (x < -1e4f) x = -1e4f;
         const float sum = hi + x, bb = sum - hi;
         lo += (hi - (sum - bb)) + (x - bb);
         hi = sum;

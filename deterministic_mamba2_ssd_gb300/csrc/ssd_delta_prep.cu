@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(Shape s, Args a, Tile
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int t = 2 * lane + y;
-          // a decay to nothing stays a finite number: exp(-1e4) is zero all the same
-          const float x = t < n ? fmaxf(a.g[(b + t) * s.H + h], -1e4f) : 0.f;
+          // a decay to nothing stays a finite number: exp(-1e4) is zero all the same (and a NaN a NaN)
+          float x = t < n ? a.g[(b + t) * s.H + h] : 0.f;
+          if (x < -1e4f) x = -1e4f;
           v[y] = __fmul_rn(x, kLog2e);
           vl[y] = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -v[y]));
           sm.beta[warp][t] = t < n ? a.beta[(b + t) * s.H + h] : 0.f;

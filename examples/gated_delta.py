@@ -1,0 +1,127 @@
+#!/usr/bin/env python
+"""A layer of linear attention by the gated delta rule, trained and served.
+
+Projections (library matrix products) -> norm and rotation of queries and keys
+(qk_norm) -> gated delta rule (delta) -> z-gate -> projection.  Trains the
+layer for a few steps to reproduce a fixed teacher layer on packed sequences;
+then serves it: the prompts are prefilled into a pool of states (delta_prefill)
+and continued token by token (qk_fwd, delta_step, gate_fwd), which has to give
+what the whole sequences give at once.
+
+    python examples/gated_delta.py [--steps 20] [--tokens 512]
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."))
+
+import torch  # noqa: E402
+
+import deterministic_mamba2_ssd_gb300 as ssd  # noqa: E402
+
+
+class Layer(torch.nn.Module):
+    """width -> width; `heads` of headdim values, in `groups` that share queries and keys of dstate elements."""
+
+    def __init__(self, width=256, heads=8, headdim=64, groups=4, dstate=64, positions=4096, seed=0):
+        super().__init__()
+        self.shape = heads, headdim, groups, dstate
+        self.split = [groups * dstate, groups * dstate, heads * headdim, heads * headdim, heads, heads]
+        gen = torch.Generator().manual_seed(seed)
+        w = torch.randn(sum(self.split), width, generator=gen) * width ** -0.5
+        self.w_in = torch.nn.Parameter(w.cuda())
+        self.w_out = torch.nn.Parameter((torch.randn(width, heads * headdim, generator=gen) * (heads * headdim) ** -0.5).cuda())
+        self.a_log = torch.nn.Parameter(torch.linspace(-3, 0, heads).cuda())   # decays of many lengths
+        angle = torch.arange(positions)[:, None] * 1e4 ** (-torch.arange(0, dstate // 4) / (dstate // 4))
+        self.cos, self.sin = angle.cos().float().cuda(), angle.sin().float().cuda()
+
+    def project(self, x):
+        """q, k (slices of one row each), v, z and the fp32 log decays and step sizes of x (b, T, width)."""
+        H, P, G, N = self.shape
+        y = x @ self.w_in.to(x.dtype).t()
+        q, k, v, z, a, b = y.split(self.split, dim=-1)
+        g = -self.a_log.exp() * torch.nn.functional.softplus(a.float())
+        return (q.unflatten(-1, (G, N)), k.unflatten(-1, (G, N)), v.unflatten(-1, (H, P)), z.contiguous(), g,
+                torch.sigmoid(b.float()).contiguous())
+
+    def forward(self, x, positions, cu_seqlens=None):
+        q, k, v, z, g, beta = self.project(x)
+        q, k = ssd.qk_norm(q, k, cos=self.cos, sin=self.sin, positions=positions)
+        o, _ = ssd.delta(q, k, v, g, beta, cu_seqlens=cu_seqlens)
+        y = o.flatten(2) * torch.nn.functional.silu(z)
+        return y @ self.w_out.to(x.dtype).t()
+
+    @torch.no_grad()
+    def prefill(self, x, positions, cu_seqlens):
+        """(y, states): the prompts packed into one row, and each one's state."""
+        q, k, v, z, g, beta = self.project(x)
+        q, k = ssd.qk_fwd(q, k, cos=self.cos, sin=self.sin, positions=positions)
+        o, states = ssd.delta_prefill(q, k, v, g, beta, cu_seqlens=cu_seqlens)
+        return ssd.gate_fwd(o.flatten(2), z).to(x.dtype) @ self.w_out.to(x.dtype).t(), states
+
+    @torch.no_grad()
+    def step(self, x, positions, pool, slots):
+        """One token of each sequence; its state in the pool goes on in place."""
+        q, k, v, z, g, beta = self.project(x)
+        q, k = ssd.qk_fwd(q, k, cos=self.cos, sin=self.sin, positions=positions)
+        o = ssd.delta_step(q, k, v, g, beta, pool, slots=slots)
+        return ssd.gate_fwd(o.flatten(2), z).to(x.dtype) @ self.w_out.to(x.dtype).t()
+
+
+def run(steps=20, tokens=512, seed=1):
+    """(losses of the training steps, relative difference of served and whole sequences)."""
+    torch.manual_seed(seed)
+    lengths = [tokens // 2, tokens // 4 + 1, tokens - tokens // 2 - tokens // 4 - 1]
+    cu = torch.tensor([0] + lengths).cumsum(0).to(device="cuda", dtype=torch.int32)
+    positions = torch.cat([torch.arange(n) for n in lengths]).to(device="cuda", dtype=torch.int32)[None]
+    teacher, layer = Layer(seed=0), Layer(seed=0)
+    with torch.no_grad():
+        for p in layer.parameters():
+            p.add_(torch.randn_like(p), alpha=0.3 * float(p.std()))
+    opt = torch.optim.Adam(layer.parameters(), lr=3e-3)
+    losses = []
+    for _ in range(steps):
+        x = torch.randn(1, tokens, 256, device="cuda").bfloat16()
+        with torch.no_grad():
+            want = teacher(x, positions, cu)
+        opt.zero_grad()
+        loss = (layer(x, positions, cu) - want).float().square().mean()
+        loss.backward()
+        opt.step()
+        losses.append(loss.item())
+    # serve: all but the last 8 tokens of each sequence as the prompt, the rest one at a time
+    x = torch.randn(1, tokens, 256, device="cuda").bfloat16()
+    with torch.no_grad():
+        whole = layer(x, positions, cu)
+    ends = cu[1:].tolist()
+    head = [slice(e - n, e - 8) for n, e in zip(lengths, ends)]
+    pcu = torch.tensor([0] + [n - 8 for n in lengths]).cumsum(0).to(device="cuda", dtype=torch.int32)
+    y, states = layer.prefill(torch.cat([x[:, s] for s in head], 1).contiguous(),
+                              torch.cat([positions[:, s] for s in head], 1).contiguous(), pcu)
+    pool = torch.zeros((5,) + states.shape[1:], device="cuda")
+    slots = torch.tensor([4, 0, 2], device="cuda", dtype=torch.int32)
+    pool[slots.long()] = states
+    got = [y[:, int(pcu[i]):int(pcu[i + 1])] for i in range(3)]
+    for t in range(8):
+        at = [e - 8 + t for e in ends]
+        y = layer.step(x[0, at][:, None].contiguous(), positions[0, at][:, None].contiguous(), pool, slots)
+        got = [torch.cat([got[i], y[i:i + 1]], 1) for i in range(3)]
+    served = torch.cat(got, 1).float()
+    return losses, float((served - whole.float()).norm() / whole.float().norm())
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--tokens", type=int, default=512)
+    a = ap.parse_args()
+    losses, diff = run(a.steps, a.tokens)
+    print("loss %.2e -> %.2e over %d steps; served against whole sequences: relative difference %.1e" %
+          (losses[0], losses[-1], a.steps, diff))
+
+
+if __name__ == "__main__":
+    main()

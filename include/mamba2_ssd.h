@@ -487,8 +487,11 @@ const char *mamba2_ssd_delta_path_name(const ssd_delta_dims *dims);
  *
  * bf16 with dstate 64 or 128 and headdim a multiple of 16 up to 128 runs the
  * tensor-core kernels ("tiles") in chunks of 64 tokens: matrix operands of 11
- * bits (22 for the state where final_states is asked for), fp32 sums.  Every
- * other shape, and fp32, runs token by token in fp32 ("general"). */
+ * bits (22 for the state where final_states is asked for), fp32 sums.  They are
+ * made for keys with which the recurrence is stable (beta |k|^2 <= 2, as after
+ * the norm above): with larger ones values may leave fp16's range, and turn
+ * into infinities, within a chunk.  Every other shape, and fp32, runs token by
+ * token in fp32 ("general"). */
 ssd_status mamba2_ssd_delta_fwd(const ssd_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
                                 const float *beta, const int32_t *cu_seqlens, const float *init_states, float scale,
                                 void *o, float *final_states, void *saved, size_t saved_bytes, void *workspace,
