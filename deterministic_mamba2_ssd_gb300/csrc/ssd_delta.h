@@ -108,5 +108,10 @@ cudaError_t general_bwd(const Shape &s, bool bf16, const Args &a, const void *sa
 cudaError_t general_step(const Shape &s, bool bf16, const Args &a, float *pool, const int32_t *slots, int64_t nslots,
                          cudaStream_t st);
 
+// Recurrences of whole sequences with few rows of state (ssd_delta_seq.cu): states entering the chunks and e where wanted, else NULL; gradients
+// of the states leaving the chunks, and F.
+cudaError_t seq_fwd(const Shape &s, bool bf16, const Args &a, float *states, float *es, cudaStream_t st);
+cudaError_t seq_bwd(const Shape &s, bool bf16, const Args &a, float *dstates, float *F, cudaStream_t st);
+
 }  // namespace delta
 }  // namespace ssd

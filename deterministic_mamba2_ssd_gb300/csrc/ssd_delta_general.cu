@@ -2,7 +2,8 @@
 // forward (whole sequences, and the in-place update of a pool of states that
 // serves single tokens), the recurrent backward of the state, and the chunk
 // kernel that turns both into the gradients.  fp32 arithmetic throughout, any
-// headdim, dstate up to 256.
+// headdim, dstate up to 256.  Whole sequences with few rows of state have
+// kernels of their own (ssd_delta_seq.cu).
 //
 // Rows of the state never mix: row p of S sees only v[p].  So a row is the
 // unit of work: 8 lanes share one, four rows a warp, sixteen a CTA, and the
@@ -11,6 +12,8 @@
 // shuffles in one fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "ssd_delta.h"
 
@@ -567,6 +570,13 @@ Work carve_work(const Shape &s, void *p) {
   return o;
 }
 
+// Whether whole sequences get a warp a row (ssd_delta_seq.cu) or eight lanes: while all of the former's CTAs of four rows
+// are on the GPU at once, two an SM, or one where dstate needs the registers or is too short to gain.  fp32, both sides,
+// forward and backward: 480 rows, dstate 72, 517 tokens 75 and 153 us, 148 and 188 with eight lanes; 1216 rows, dstate
+// 128, 400 tokens 78 and 170, 115 and 173; 2048 rows 150 and 281, 118 and 206; 1216 rows of 32 76 and 136, 81 and 118;
+// 200 rows of 200, 700 tokens 128 and 276, 237 and 360.
+bool few_rows(const Shape &s) { return s.nseq * s.H * s.P <= (s.N > 32 && s.N <= 128 ? 2 : 1) * 152 * 4; }
+
 dim3 rec_grid(const Shape &s, int rows) {
   return dim3(unsigned((s.P + rows - 1) / rows), unsigned(s.H), unsigned(s.nseq < 65535 ? s.nseq : 65535));
 }
@@ -600,11 +610,16 @@ cudaError_t launch_step(const Shape &s, const Args &a, float *pool, const int32_
 
 template <class T>
 cudaError_t launch_bwd(const Shape &s, const Args &a, const Saved &sv, const Work &w, cudaStream_t st) {
-  const dim3 grid = rec_grid(s, kRows);
-  if (s.N <= 32) rec_bwd_kernel<T, 1><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
-  else if (s.N <= 64) rec_bwd_kernel<T, 2><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
-  else if (s.N <= 128) rec_bwd_kernel<T, 4><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
-  else rec_bwd_kernel<T, 8><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+  if (few_rows(s)) {
+    const cudaError_t e = seq_bwd(s, std::is_same<T, __nv_bfloat16>::value, a, w.dstates, w.F, st);
+    if (e != cudaSuccess) return e;
+  } else {
+    const dim3 grid = rec_grid(s, kRows);
+    if (s.N <= 32) rec_bwd_kernel<T, 1><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+    else if (s.N <= 64) rec_bwd_kernel<T, 2><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+    else if (s.N <= 128) rec_bwd_kernel<T, 4><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+    else rec_bwd_kernel<T, 8><<<grid, kThreads, 0, st>>>(s, a, w.dstates, w.F);
+  }
   if (s.total == 0) return cudaGetLastError();
   const dim3 ggrid(unsigned(s.slots < (int64_t(1) << 30) ? s.slots : int64_t(1) << 30), unsigned(s.H));
   grads_kernel<T><<<ggrid, kGThreads, 0, st>>>(s, a, sv.states, sv.es, w.dstates, w.F, w.dqh, w.dkh);
@@ -622,6 +637,7 @@ size_t general_bwd_workspace(const Shape &s) { return carve_work(s, nullptr).byt
 cudaError_t general_fwd(const Shape &s, bool bf16, const Args &a, void *saved, cudaStream_t st) {
   Saved sv{};
   if (saved != nullptr) sv = carve_saved(s, saved);
+  if (few_rows(s)) return seq_fwd(s, bf16, a, sv.states, sv.es, st);
   return bf16 ? launch_fwd<__nv_bfloat16, kBlock, 1, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st)
               : launch_fwd<float, kBlock, 1, false>(s, a, sv.states, sv.es, nullptr, nullptr, 0, st);
 }
