@@ -12,10 +12,12 @@
 // Bandwidth-bound: every row is read once and written once.  A thread holds
 // the two ends of its pairs, so the rotation needs no exchange between
 // threads; only the sum of squares (and u . h) is shared, by shuffles inside
-// the lanes of one row.  Two forms of the same kernel:
+// the lanes of one row.  Three forms of the same kernel:
 //   - wide: pairs in runs of 8 consecutive elements (16-byte loads for bf16),
 //     D / 16 lanes a row; D 32, 64, 128 or 256, R a multiple of 16, rows on
 //     16-byte boundaries;
+//   - pairs: runs of 2, half a warp or a warp a row; D even, R a multiple of 4,
+//     rows on boundaries of two elements;
 //   - narrow: one pair at a time, a warp a row; any D up to 512.
 // A CTA takes a tile of consecutive tokens and a range of the heads of q or of
 // k, so that a token's cos and sin are read once for all of them; the heads
@@ -64,6 +66,11 @@ struct Run {
   __device__ __forceinline__ void load(const T *p, bool on) {
     if constexpr (V == 1) {
       w[0] = on ? __float_as_uint(ld(p)) : 0u;
+    } else if constexpr (V == 2 && sizeof(T) == 2) {
+      w[0] = on ? *reinterpret_cast<const uint32_t *>(p) : 0u;
+    } else if constexpr (V == 2) {
+      const uint2 u = on ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
+      w[0] = u.x, w[1] = u.y;
     } else {
 #pragma unroll
       for (int i = 0; i < int(V * sizeof(T) / 16); ++i) {
@@ -84,6 +91,10 @@ template <int V, class T>
 __device__ __forceinline__ void store_run(T *p, const float (&v)[V]) {
   if constexpr (V == 1) {
     ssd::st(p, v[0]);
+  } else if constexpr (V == 2 && sizeof(T) == 2) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
   } else if constexpr (sizeof(T) == 2) {
     uint32_t w[4];
 #pragma unroll
@@ -335,9 +346,19 @@ void launch(const Params &q, dim3 blocks, bool has_w, cudaStream_t st) {
   else qk_kernel<T, V, L, PT, kBwd, false><<<blocks, kThreads, 0, st>>>(q);
 }
 
+// Elements of a run, and lanes of a row.
+enum Form { kNarrow = 1, kPairs = 2, kWide = 8 };
+int lanes_of(Form form, int D) { return form == kWide ? D / 16 : form == kPairs && D <= 64 ? 16 : 32; }
+
 template <class T, bool kBwd>
-void launch_form(const Params &q, bool wide, dim3 blocks, bool has_w, cudaStream_t st) {
-  if (wide) {
+void launch_form(const Params &q, Form form, dim3 blocks, bool has_w, cudaStream_t st) {
+  if (form == kPairs) {
+    if (q.D <= 64) return launch<T, 2, 16, 1, kBwd>(q, blocks, has_w, st);
+    if (q.D <= 128) return launch<T, 2, 32, 1, kBwd>(q, blocks, has_w, st);
+    if (q.D <= 256) return launch<T, 2, 32, 2, kBwd>(q, blocks, has_w, st);
+    return launch<T, 2, 32, 4, kBwd>(q, blocks, has_w, st);
+  }
+  if (form == kWide) {
     switch (q.D) {
       case 32: return launch<T, 8, 2, 1, kBwd>(q, blocks, has_w, st);
       case 64: return launch<T, 8, 4, 1, kBwd>(q, blocks, has_w, st);
@@ -352,6 +373,7 @@ void launch_form(const Params &q, bool wide, dim3 blocks, bool has_w, cudaStream
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 bool dims_ok(const ssd_qk_dims *d) {
   if (d == nullptr || d->tokens < 0 || d->qheads < 1 || d->kheads < 1 || d->headdim < 1 || d->headdim > 512)
@@ -418,10 +440,15 @@ ssd_status run(const ssd_qk_dims *d, bool bwd, const void *q, const void *k, con
   const bool wide = (D == 32 || D == 64 || D == 128 || D == 256) && d->rotary % 16 == 0 && aligned16(q) &&
                     aligned16(k) && aligned16(oq) && aligned16(ok) && aligned16(dq_in) && aligned16(dk_in) &&
                     aligned16(cos) && aligned16(sin) && size_t(qs) * el % 16 == 0 && size_t(ks) * el % 16 == 0;
-  const int groups = wide ? kThreads / (D / 16) : kThreads / 32;
+  const size_t two = 2 * el;
+  const bool pairs = D % 2 == 0 && d->rotary % 4 == 0 && qs % 2 == 0 && ks % 2 == 0 && aligned_to(q, two) &&
+                     aligned_to(k, two) && aligned_to(oq, two) && aligned_to(ok, two) && aligned_to(dq_in, two) &&
+                     aligned_to(dk_in, two) && aligned_to(cos, 8) && aligned_to(sin, 8);
+  const Form form = wide ? kWide : pairs ? kPairs : kNarrow;
+  const int groups = kThreads / lanes_of(form, D);
   const int64_t tiles = (d->tokens + groups - 1) / groups;
   auto ranges = [&](int heads) {   // enough that tiles * ranges fill the GPU, half for each side
-    const int64_t sets = wide ? (heads + kHeads - 1) / kHeads : heads;
+    const int64_t sets = form == kNarrow ? heads : (heads + kHeads - 1) / kHeads;
     const int64_t want = (kFill / 2 + tiles - 1) / tiles;
     return int(want < sets ? want : sets);
   };
@@ -438,11 +465,11 @@ ssd_status run(const ssd_qk_dims *d, bool bwd, const void *q, const void *k, con
   }
   const dim3 blocks(unsigned(columns), unsigned(p.ranges0 + ranges1));
   if (d->dtype == SSD_BF16) {
-    if (bwd) launch_form<__nv_bfloat16, true>(p, wide, blocks, has_w, st);
-    else launch_form<__nv_bfloat16, false>(p, wide, blocks, has_w, st);
+    if (bwd) launch_form<__nv_bfloat16, true>(p, form, blocks, has_w, st);
+    else launch_form<__nv_bfloat16, false>(p, form, blocks, has_w, st);
   } else {
-    if (bwd) launch_form<float, true>(p, wide, blocks, has_w, st);
-    else launch_form<float, false>(p, wide, blocks, has_w, st);
+    if (bwd) launch_form<float, true>(p, form, blocks, has_w, st);
+    else launch_form<float, false>(p, form, blocks, has_w, st);
   }
   if (bwd && has_w)
     weight_fold_kernel<<<dim3(unsigned((D + 7) / 8), 2), 256, 0, st>>>(p.side[0].part, p.side[1].part,
