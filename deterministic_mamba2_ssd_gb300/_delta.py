@@ -72,14 +72,19 @@ def delta_path_name(dims: DeltaDims) -> str:
 def _scope(device, stream):
     """(context, stream handle) in which a call on `device` allocates and launches."""
     if stream is None:
-        s = torch.cuda.current_stream(device)
         if device.index == torch.cuda.current_device():
-            return _HERE, s.cuda_stream
-        return torch.cuda.stream(s), s.cuda_stream
+            return _HERE, _raw_stream(device.index)   # the handle alone: a Stream object costs as much as a launch
+        stream = torch.cuda.current_stream(device)
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
 _HERE = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _packed(t):
+    """An uninitialised tensor of t's shape and type, packed."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 # What the checks of arguments look at.  A call's checks, struct and sizes depend on nothing else, so they are made once
@@ -195,8 +200,7 @@ def qk_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, norm="l2"
                   None, None, norm, eps, interleaved)[1]
     ctx, st = _scope(q.device, stream)
     with ctx:
-        yq = q.new_empty(q.shape)
-        yk = k.new_empty(k.shape)
+        yq, yk = _packed(q), _packed(k)
         rc = lib().mamba2_ssd_qk_fwd(at, q.data_ptr(), k.data_ptr(), _at(wq), _at(wk), _at(cos), _at(sin),
                                      _at(positions), yq.data_ptr(), yk.data_ptr(), st)
     if rc:
@@ -214,7 +218,7 @@ def qk_bwd(q, k, dyq, dyk, wq=None, wk=None, cos=None, sin=None, positions=None,
     dt, dev = q.dtype, q.device
     ctx, st = _scope(dev, stream)
     with ctx:
-        out = dict(dq=q.new_empty(q.shape), dk=k.new_empty(k.shape))
+        out = dict(dq=_packed(q), dk=_packed(k))
         ws = None
         if wq is not None:
             out["dwq"], out["dwk"] = torch.empty_like(wq), torch.empty_like(wk)
@@ -306,7 +310,7 @@ def _delta_run(q, k, v, g, beta, scale, cu_seqlens, init_states, want_final, wan
     dev = q.device
     ctx, st = _scope(dev, stream)
     with ctx:
-        o = v.new_empty(v.shape)
+        o = _packed(v)
         final = torch.empty((dims.nseq, dims.nheads, dims.headdim, dims.dstate), dtype=torch.float32,
                             device=dev) if want_final else None
         saved = torch.empty(saved_bytes, dtype=torch.uint8, device=dev) if want_saved else None
@@ -316,6 +320,8 @@ def _delta_run(q, k, v, g, beta, scale, cu_seqlens, init_states, want_final, wan
                                         saved_bytes if want_saved else 0, _at(ws), 0 if want_saved else ws_bytes, st)
     if rc:
         raise SsdError(rc, "mamba2_ssd_delta_fwd")
+    if not want_saved:
+        return o, final, None
     keep = dict(q=q, k=k, g=g, beta=beta, cu_seqlens=cu_seqlens, init=init_states, saved=saved, final=final)
     return o, final, DeltaSaved(plan, keep, scale)
 
@@ -351,7 +357,7 @@ def delta_bwd(saved: DeltaSaved, dout, dfinal=None, want_dinit=None, stream=None
     _, at, saved_bytes, _, need = saved.plan
     ctx, st = _scope(dev, stream)
     with ctx:
-        out = dict(dq=q.new_empty(q.shape), dk=k.new_empty(k.shape),
+        out = dict(dq=_packed(q), dk=_packed(k),
                    dv=torch.empty(shape, dtype=dt, device=dev), dg=torch.empty(shape[:3], dtype=dt, device=dev),
                    dbeta=torch.empty(shape[:3], dtype=dt, device=dev))
         if want_dinit:
@@ -389,7 +395,7 @@ def delta_step(q, k, v, g, beta, states, slots=None, scale=None, stream=None):
     scale = dims.dstate ** -0.5 if scale is None else float(scale)
     ctx, st = _scope(q.device, stream)
     with ctx:
-        o = v.new_empty(v.shape)
+        o = _packed(v)
         rc = lib().mamba2_ssd_delta_step(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                          scale, states.data_ptr(), states.shape[0], _at(slots), o.data_ptr(), st)
     if rc:
