@@ -102,10 +102,6 @@ __device__ __forceinline__ float pow2_inv(float s) { return __uint_as_float(0x7F
 __device__ __forceinline__ uint32_t b_addr(uint32_t tile, int n0, int k0, int bytes, int lane) {
   return tile + swz(n0 + (lane & 7) + ((lane >> 4) << 3), (k0 >> 3) + ((lane >> 3) & 1), bytes);
 }
-// The same operands from a tile [k][n] (transposing load): matrices (k0, n0), (k0+8, n0), (k0, n0+8), (k0+8, n0+8).
-__device__ __forceinline__ uint32_t bt_addr(uint32_t tile, int n0, int k0, int bytes, int lane) {
-  return tile + swz(k0 + (lane & 7) + (((lane >> 3) & 1) << 3), (n0 >> 3) + (lane >> 4), bytes);
-}
 // A operand 16 x 16 at (m0, k0) of a tile [m][k].
 __device__ __forceinline__ uint32_t a_addr(uint32_t tile, int m0, int k0, int bytes, int lane) {
   return tile + swz(m0 + (lane & 7) + (((lane >> 3) & 1) << 3), (k0 >> 3) + (lane >> 4), bytes);
