@@ -137,6 +137,13 @@ struct Tile {
   }
 };
 
+// The step is bounded by reading and writing the states: 192 sequences of 32
+// heads of 128 x 128 take 121 us (127 with the call, 94% of the measured copy
+// rate); four tokens each of 48 sequences of 64 heads of 64 x 128 take 46, since
+// a state waits for its four tokens between.  Whole sequences with many rows are
+// bounded by the order of their tokens and the sums over the lanes: 400 tokens
+// of 4096 rows of 128 in fp32 take 136 us.
+//
 // CTA (16 RS rows of the state, head, sequence), tokens in order.  With RS 2 a
 // group of lanes has two rows, 16 apart: twice the loads in flight where there
 // are states enough to fill the GPU.

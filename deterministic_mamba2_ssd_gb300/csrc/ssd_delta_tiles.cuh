@@ -14,7 +14,8 @@
 //                            (zero above the diagonal; there, only the 16 x 16
 //                            blocks (0, 1) and (2, 3) are written)
 //   vec (slot, head):        kVec floats, see the offsets below
-//   S16 (slot, head):        state entering the chunk, rows [p][n] times 2^-r
+//   S16 (slot, head):        state entering the chunk, rows [p][n], over 2^r
+//                            and the chunk's unit (kVecUnit)
 //   E16 (slot, head):        e of the chunk, rows [t][p] (not swizzled) times 2^-r
 //   up  (slot, head):        2^r, one for each strip of 16 p
 // and from the backward chain, with scales ub of its own: D16 like S16, the

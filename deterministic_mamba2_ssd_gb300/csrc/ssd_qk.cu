@@ -24,6 +24,10 @@
 // are cut into as many ranges as it takes to fill the GPU when tokens are few.
 // Loads of kHeads heads are in flight at once in each of 3 (backward: 2) CTAs
 // an SM.
+//
+// Bounded by bandwidth: 32768 tokens of 48 heads of 128 in bf16, forward 143 us
+// (83% of the measured copy rate), backward with weights 227 (78%).  Pairs in
+// place of narrow, 9345 tokens of 16 heads of 158: 36 and 56 us, 80 and 115.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
